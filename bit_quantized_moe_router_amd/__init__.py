@@ -23,6 +23,8 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_BAD
 MOE_Q_TERNARY, MOE_Q_INT2, MOE_Q_INT3 = 1, 2, 3
 MOE_LOGITS_GIVEN, MOE_ADD_RESIDUAL = 1, 2
 MOE_MAX_DECODE_TOKENS = 8
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 1, 2
+MOE_MAX_GROUPS = 64
 MOE_DECODE_STAGE_ROUTE, MOE_DECODE_STAGE_SELECT, MOE_DECODE_STAGE_GATEUP, MOE_DECODE_STAGE_DOWN = \
     1, 2, 4, 8
 MOE_DECODE_STAGES_ALL = 15
@@ -35,6 +37,7 @@ EXPORTED = ("moe_packed_bytes", "moe_expert_bytes", "moe_pack_weights", "moe_qua
             "moe_requantize", "moe_workspace_bytes",
             "moe_route_topk", "moe_forward_decode", "moe_forward_prefill",
             "moe_forward_decode_stages", "moe_forward_prefill_stages",
+            "moe_route_scored", "moe_forward_decode_scored", "moe_forward_prefill_scored",
             "moe_forward_decode_noalloc", "moe_status_string", "moe_abi_version")
 
 
@@ -62,6 +65,13 @@ class moe_routing(ctypes.Structure):
                 ("topk_w", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("offsets", ctypes.c_void_p), ("perm_tok", ctypes.c_void_p),
                 ("inv_row", ctypes.c_void_p)]
+
+
+class moe_scoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("choice_bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -96,7 +106,12 @@ def load():
     lib.moe_forward_decode_stages.argtypes = [L, vp, ctypes.c_int32, u32, R, vp, sz, vp, u32, vp]
     lib.moe_forward_prefill_stages.argtypes = [L, vp, ctypes.c_int32, u32, R, vp, sz, vp, u32, vp]
     lib.moe_forward_decode_noalloc.argtypes = [L, vp, ctypes.c_int32, u32, R, vp, vp]
-    for f in (lib.moe_route_topk, lib.moe_forward_decode, lib.moe_forward_prefill,
+    S = ctypes.POINTER(moe_scoring)
+    lib.moe_route_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp]
+    lib.moe_forward_decode_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp, vp]
+    lib.moe_forward_prefill_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp, vp]
+    for f in (lib.moe_route_scored, lib.moe_forward_decode_scored, lib.moe_forward_prefill_scored,
+              lib.moe_route_topk, lib.moe_forward_decode, lib.moe_forward_prefill,
               lib.moe_forward_decode_stages, lib.moe_forward_prefill_stages,
               lib.moe_forward_decode_noalloc):
         f.restype = i32
@@ -289,6 +304,51 @@ def moe_forward_prefill_stages(layer: Layer, x, T: int, flags: int, routing: Rou
                                            0 if ws is None else ws.numel(), _ptr(out),
                                            stage_mask, _stream(stream))
     _check(st, "moe_forward_prefill_stages")
+
+
+# -------------------------------------------------- routing by scores
+@dataclass
+class Scoring:
+    """A moe_scoring plus the bias tensor it points into (kept alive here)."""
+    c: moe_scoring
+    choice_bias: torch.Tensor | None
+
+
+def make_scoring(score: int, n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                 renorm: bool = True, scale: float = 1.0, choice_bias=None) -> Scoring:
+    """A router by scores (MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID); choice_bias: device fp32 [E]
+    added to the scores for the choice only."""
+    if isinstance(choice_bias, torch.Tensor) and (choice_bias.dtype != torch.float32
+                                                  or not choice_bias.is_contiguous()):
+        raise MoeError(MOE_ERR_INVALID_ARG, "make_scoring: choice_bias must be contiguous float32")
+    return Scoring(moe_scoring(score, n_groups, topk_groups, group_top, int(renorm), scale,
+                               _ptr(choice_bias)), choice_bias)
+
+
+def moe_route_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int, routing: Routing, ws,
+                     stream=None):
+    st = load().moe_route_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x), T, flags,
+                                 ctypes.byref(routing.c), _ptr(ws),
+                                 0 if ws is None else ws.numel(), _stream(stream))
+    _check(st, "moe_route_scored")
+
+
+def moe_forward_decode_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int,
+                              routing: Routing, ws, out, stream=None):
+    st = load().moe_forward_decode_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x),
+                                          T, flags, ctypes.byref(routing.c), _ptr(ws),
+                                          0 if ws is None else ws.numel(), _ptr(out),
+                                          _stream(stream))
+    _check(st, "moe_forward_decode_scored")
+
+
+def moe_forward_prefill_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int,
+                               routing: Routing, ws, out, stream=None):
+    st = load().moe_forward_prefill_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x),
+                                           T, flags, ctypes.byref(routing.c), _ptr(ws),
+                                           0 if ws is None else ws.numel(), _ptr(out),
+                                           _stream(stream))
+    _check(st, "moe_forward_prefill_scored")
 
 
 def moe_abi_version() -> int:

@@ -1,5 +1,6 @@
 // C ABI entry points: argument validation, workspace layout, dispatch.
 // Every check below happens before anything is enqueued on the stream.
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -78,6 +79,22 @@ PrefillWs prefill_ws_layout(const moe_layer* L, int T) {
   return p;
 }
 
+// The routing by scores keeps the tile list where PrefillWs has it and its own
+// scratch behind it, in regions that the layer fills after routing.
+static size_t scored_ws_need(const moe_layer* L, int T) {
+  return prefill_ws_layout(L, T).xs + scored_ws_bytes(L, T);
+}
+
+// what moe_route_topk and the forward calls need
+static size_t base_ws_need(const moe_layer* L, int T) {
+  size_t b = prefill_ws_layout(L, T).total;
+  if (T <= MOE_MAX_DECODE_TOKENS) {
+    const size_t dcd = decode_ws_layout(L, T).total;
+    if (dcd > b) b = dcd;
+  }
+  return b;
+}
+
 static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + nb && y < x + na;
@@ -86,7 +103,7 @@ static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 // shared checks for the calls that take routing buffers
-// (ws_need: the workspace bytes the call requires; 0 = moe_workspace_bytes(L, T))
+// (ws_need: the workspace bytes the call requires; 0 = base_ws_need(L, T))
 static moe_status check_common(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
                                const moe_routing* R, const void* ws, size_t ws_bytes,
                                bool need_experts, size_t ws_need = 0) {
@@ -123,7 +140,8 @@ static moe_status check_common(const moe_layer* L, const uint16_t* x, int32_t T,
         return MOE_ERR_INVALID_ARG;
     }
   }
-  if (!ws || ws_bytes < (ws_need ? ws_need : moe_workspace_bytes(L, T))) return MOE_ERR_WORKSPACE;
+  if (!ws) return MOE_ERR_WORKSPACE;
+  if (T > 0 && ws_bytes < (ws_need ? ws_need : base_ws_need(L, T))) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -135,12 +153,8 @@ using namespace bqmoe;
 extern "C" size_t moe_workspace_bytes(const moe_layer* L, int32_t T) {
   if (!layer_ok(L) || T < 0) return 0;
   if (T == 0) return 256;
-  size_t b = prefill_ws_layout(L, T).total;
-  if (T <= MOE_MAX_DECODE_TOKENS) {
-    const size_t dcd = decode_ws_layout(L, T).total;
-    if (dcd > b) b = dcd;
-  }
-  return b;
+  const size_t b = base_ws_need(L, T), s = scored_ws_need(L, T);
+  return b > s ? b : s;
 }
 
 extern "C" moe_status moe_route_topk(const moe_layer* L, const uint16_t* x, int32_t T,
@@ -157,9 +171,9 @@ extern "C" moe_status moe_route_topk(const moe_layer* L, const uint16_t* x, int3
 namespace bqmoe {
 // decode_ws_only: the workspace need only hold the decode layout (the
 // no-allocation entry point's fixed array), not moe_workspace_bytes
-moe_status decode_call(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
-                       moe_routing* R, void* ws, size_t ws_bytes, uint16_t* out, uint32_t mask,
-                       void* stream, bool decode_ws_only) {
+static moe_status check_decode(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
+                               const moe_routing* R, const void* ws, size_t ws_bytes,
+                               const uint16_t* out, bool decode_ws_only) {
   if (T < 1 || T > MOE_MAX_DECODE_TOKENS) return MOE_ERR_INVALID_ARG;
   if (decode_ws_only && !layer_ok(L)) return L ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG;
   const size_t need = decode_ws_only ? decode_ws_layout(L, T).total : 0;
@@ -171,9 +185,36 @@ moe_status decode_call(const moe_layer* L, const uint16_t* x, int32_t T, uint32_
   if (!out || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
   const size_t bytes = (size_t)T * L->d * 2;
   if (overlaps(x, bytes, out, bytes)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status decode_call(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
+                       moe_routing* R, void* ws, size_t ws_bytes, uint16_t* out, uint32_t mask,
+                       void* stream, bool decode_ws_only) {
+  const moe_status st = check_decode(L, x, T, flags, R, ws, ws_bytes, out, decode_ws_only);
+  if (st != MOE_OK) return st;
   const DecodeWs W = decode_ws_layout(L, T);
   return launch_decode(L, x, T, flags, R, (uint8_t*)ws, W, out, stream, mask) ? MOE_ERR_DEVICE
                                                                             : MOE_OK;
+}
+
+// ws_need as in check_common
+static moe_status check_prefill(const moe_layer* L, const uint16_t* x, int32_t T, uint32_t flags,
+                                const moe_routing* R, const void* ws, size_t ws_bytes,
+                                const uint16_t* out, size_t ws_need) {
+  moe_status st = check_common(L, x, T, flags, R, ws, ws_bytes, true, ws_need);
+  if (st != MOE_OK) return st;
+  if (L->alt_experts) return MOE_ERR_UNSUPPORTED;  // the second expert copy is read by decode
+  if (L->d % 256) return MOE_ERR_UNSUPPORTED;  // the down GEMMs cover 256 columns per block
+  if (!out || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)T * L->d * 2;
+  if (overlaps(x, bytes, out, bytes)) return MOE_ERR_INVALID_ARG;
+  const PrefillWs P = prefill_ws_layout(L, T);
+  // the 2-bit and ternary kernels address their activation rows with 32-bit byte offsets
+  if ((prefill_x2(L) || prefill_exact16(L)) && (size_t)P.rows * (size_t)(L->d > L->inter ? L->d : L->inter) * 2 >
+                           (size_t)UINT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 }  // namespace bqmoe
 
@@ -187,18 +228,9 @@ static moe_status prefill_impl(const moe_layer* L, const uint16_t* x, int32_t T,
                                moe_routing* R, void* ws, size_t ws_bytes, uint16_t* out,
                                uint32_t mask, void* stream) {
   if (T == 0 && L && R) return MOE_OK;
-  moe_status st = check_common(L, x, T, flags, R, ws, ws_bytes, true);
+  const moe_status st = check_prefill(L, x, T, flags, R, ws, ws_bytes, out, 0);
   if (st != MOE_OK) return st;
-  if (L->alt_experts) return MOE_ERR_UNSUPPORTED;  // the second expert copy is read by decode
-  if (L->d % 256) return MOE_ERR_UNSUPPORTED;  // the down GEMMs cover 256 columns per block
-  if (!out || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
-  const size_t bytes = (size_t)T * L->d * 2;
-  if (overlaps(x, bytes, out, bytes)) return MOE_ERR_INVALID_ARG;
   const PrefillWs P = prefill_ws_layout(L, T);
-  // the 2-bit and ternary kernels address their activation rows with 32-bit byte offsets
-  if ((prefill_x2(L) || prefill_exact16(L)) && (size_t)P.rows * (size_t)(L->d > L->inter ? L->d : L->inter) * 2 >
-                           (size_t)UINT32_MAX)
-    return MOE_ERR_UNSUPPORTED;
   return launch_prefill(L, x, T, flags, R, (uint8_t*)ws, P, out, stream, mask) ? MOE_ERR_DEVICE
                                                                              : MOE_OK;
 }
@@ -229,6 +261,89 @@ extern "C" moe_status moe_forward_prefill_stages(const moe_layer* L, const uint1
                                                  uint32_t stage_mask, void* stream) {
   if (stage_mask == 0 || (stage_mask & ~(uint32_t)MOE_PREFILL_STAGES_ALL)) return MOE_ERR_INVALID_ARG;
   return prefill_impl(L, x, T, flags, R, ws, ws_bytes, out, stage_mask, stream);
+}
+
+// ------------------------------------------------------- routing by scores
+namespace bqmoe {
+static bool scoring_ok(const moe_layer* L, const moe_scoring* S) {
+  if (!L || !S || L->n_experts < 1 || L->top_k < 1) return false;
+  if (S->score != MOE_SCORE_SOFTMAX && S->score != MOE_SCORE_SIGMOID) return false;
+  if (S->n_groups < 1 || S->n_groups > MOE_MAX_GROUPS || L->n_experts % S->n_groups) return false;
+  const int gs = L->n_experts / S->n_groups;
+  if (S->topk_groups < 1 || S->topk_groups > S->n_groups) return false;
+  if (S->group_top < 1 || S->group_top > 2 || S->group_top > gs) return false;
+  if ((int64_t)S->topk_groups * gs < L->top_k) return false;
+  if (S->renorm != 0 && S->renorm != 1) return false;
+  return std::isfinite(S->scale) && aligned(S->choice_bias, 4);
+}
+
+// the scored routing on logits that are in R already; tiles: the grouped GEMMs' list too
+static int route_scored(const moe_layer* L, const moe_scoring* S, int T, moe_routing* R,
+                        uint8_t* ws, bool tiles, void* stream) {
+  const PrefillWs P = prefill_ws_layout(L, T);
+  ScoreOut O{};
+  O.n_shared = L->n_shared;
+  if (tiles) {
+    O.tiles = (int32_t*)(ws + P.tiles);
+    O.ctrl = (int32_t*)(ws + P.ctrl);
+    O.tm = prefill_tile_rows(L);
+  }
+  return launch_route_scored(L, S, T, R, ws + P.xs, O, stream);
+}
+}  // namespace bqmoe
+
+extern "C" moe_status moe_route_scored(const moe_layer* L, const moe_scoring* S, const uint16_t* x,
+                                       int32_t T, uint32_t flags, moe_routing* R, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  if (!scoring_ok(L, S)) return MOE_ERR_INVALID_ARG;
+  if (T == 0 && R) return MOE_OK;
+  const size_t need = layer_ok(L) && T > 0 ? scored_ws_need(L, T) : 0;
+  const moe_status st = check_common(L, x, T, flags, R, ws, ws_bytes, false, need);
+  if (st != MOE_OK) return st;
+  if (!(flags & MOE_LOGITS_GIVEN) && launch_router_logits(L, x, T, R, stream))
+    return MOE_ERR_DEVICE;
+  return route_scored(L, S, T, R, (uint8_t*)ws, false, stream) ? MOE_ERR_DEVICE : MOE_OK;
+}
+
+extern "C" moe_status moe_forward_decode_scored(const moe_layer* L, const moe_scoring* S,
+                                                const uint16_t* x, int32_t T, uint32_t flags,
+                                                moe_routing* R, void* ws, size_t ws_bytes,
+                                                uint16_t* out, void* stream) {
+  if (!scoring_ok(L, S)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_decode(L, x, T, flags, R, ws, ws_bytes, out, false);
+  if (st != MOE_OK) return st;
+  const DecodeWs W = decode_ws_layout(L, T);
+  uint8_t* w = (uint8_t*)ws;
+  if (launch_decode_route(L, x, T, flags, R, w, W, stream, MOE_DECODE_STAGE_ROUTE))
+    return MOE_ERR_DEVICE;
+  ScoreOut O{};
+  O.n_shared = L->n_shared;
+  O.slots = (int32_t*)(w + W.slots);
+  O.max_slots = W.max_slots;
+  O.alt_select = L->alt_experts ? L->alt_select : nullptr;
+  if (launch_route_scored(L, S, T, R, nullptr, O, stream)) return MOE_ERR_DEVICE;
+  return launch_decode(L, x, T, flags, R, w, W, out, stream,
+                       MOE_DECODE_STAGE_GATEUP | MOE_DECODE_STAGE_DOWN, true)
+             ? MOE_ERR_DEVICE
+             : MOE_OK;
+}
+
+extern "C" moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_scoring* S,
+                                                 const uint16_t* x, int32_t T, uint32_t flags,
+                                                 moe_routing* R, void* ws, size_t ws_bytes,
+                                                 uint16_t* out, void* stream) {
+  if (!scoring_ok(L, S)) return MOE_ERR_INVALID_ARG;
+  if (T == 0 && R) return MOE_OK;
+  const size_t need = layer_ok(L) && T > 0 ? moe_workspace_bytes(L, T) : 0;
+  const moe_status st = check_prefill(L, x, T, flags, R, ws, ws_bytes, out, need);
+  if (st != MOE_OK) return st;
+  if (!(flags & MOE_LOGITS_GIVEN) && launch_router_logits(L, x, T, R, stream))
+    return MOE_ERR_DEVICE;
+  if (route_scored(L, S, T, R, (uint8_t*)ws, true, stream)) return MOE_ERR_DEVICE;
+  return launch_prefill(L, x, T, flags, R, (uint8_t*)ws, prefill_ws_layout(L, T), out, stream,
+                        MOE_PREFILL_STAGES_ALL & ~(uint32_t)MOE_PREFILL_STAGE_ROUTE)
+             ? MOE_ERR_DEVICE
+             : MOE_OK;
 }
 
 extern "C" const char* moe_status_string(moe_status s) {

@@ -1144,11 +1144,13 @@ static int launch_gateup(const moe_layer* L, DecShape sh, int nb, int Mmax, hipS
 }
 
 int launch_decode(const moe_layer* L, const uint16_t* x, int T, uint32_t flags, moe_routing* R,
-                  uint8_t* ws, const DecodeWs& W, uint16_t* out, void* stream, uint32_t mask) {
+                  uint8_t* ws, const DecodeWs& W, uint16_t* out, void* stream, uint32_t mask,
+                  bool selected) {
   // with a second expert copy the selection stays in the select kernel, whose
   // slot records say which copy each slot reads
   const bool has_alt = L->alt_experts != nullptr;
-  const bool fused_select = select_in_gateup(L, T) && (mask & MOE_DECODE_STAGE_GATEUP) && !has_alt;
+  const bool fused_select =
+      select_in_gateup(L, T) && (mask & MOE_DECODE_STAGE_GATEUP) && !has_alt && !selected;
   int rc = launch_decode_route(L, x, T, flags, R, ws, W, stream,
                                fused_select ? mask & ~(uint32_t)MOE_DECODE_STAGE_SELECT : mask);
   if (rc) return rc;

@@ -85,11 +85,46 @@ PrefillWs prefill_ws_layout(const moe_layer* L, int T);
 int launch_route_generic(const moe_layer* L, const uint16_t* x, int T, uint32_t flags,
                          moe_routing* R, uint8_t* ws, const PrefillWs& P, void* stream);
 // `mask` selects the kernels to enqueue (bit i = stage i, see moe.h); ~0u runs all.
+// router logits of any number of tokens into R->logits
+int launch_router_logits(const moe_layer* L, const uint16_t* x, int T, moe_routing* R,
+                         void* stream);
+// Routing by scores.  What the kernels take of moe_scoring, and where they
+// write: the routing outputs and, each where its pointer is set, the decode
+// slot list (T <= 8) and the grouped GEMMs' tile list.
+struct ScoreArgs {
+  const float* bias;
+  float scale;
+  int32_t E, k, sigmoid, renorm;
+  int32_t n_groups, topk_groups, group_top, group_size;
+  uint32_t group_magic;  // (e * group_magic) >> 20 == e / group_size for e < 1024
+  int32_t team_log2;     // log2 of the lanes that look at one group
+  int32_t bits;          // bits of an expert id
+};
+struct ScoreOut {
+  int32_t* ids;
+  float* w;
+  int32_t *counts, *offsets, *perm_tok, *inv_row;
+  int32_t* slots;
+  int32_t max_slots, n_shared;
+  const uint8_t* alt_select;
+  int32_t *tiles, *ctrl;
+  int32_t tm;  // rows per tile
+};
+constexpr int kScoredFewTokens = 32;  // tokens and rows that one block routes
+constexpr int kScoredFewRows = 1024;
+size_t scored_ws_bytes(const moe_layer* L, int T);  // scratch of launch_route_scored
+int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_routing* R,
+                        uint8_t* scratch, const ScoreOut& out, void* stream);
+int launch_decode_route(const moe_layer* L, const uint16_t* x, int T, uint32_t flags,
+                        moe_routing* R, uint8_t* ws, const DecodeWs& W, void* stream,
+                        uint32_t mask);
 // Whether the decode kernels take this layer for T tokens (LDS and register
 // limits of their launch shapes).
 bool decode_shape_ok(const moe_layer* L, int T);
+// (`selected`: R and the slot list are already made, by another router)
 int launch_decode(const moe_layer* L, const uint16_t* x, int T, uint32_t flags, moe_routing* R,
-                  uint8_t* ws, const DecodeWs& W, uint16_t* out, void* stream, uint32_t mask);
+                  uint8_t* ws, const DecodeWs& W, uint16_t* out, void* stream, uint32_t mask,
+                  bool selected = false);
 int launch_prefill(const moe_layer* L, const uint16_t* x, int T, uint32_t flags, moe_routing* R,
                    uint8_t* ws, const PrefillWs& P, uint16_t* out, void* stream, uint32_t mask);
 // Prefill on exact fp16 terms (all projections ternary): the stages after routing

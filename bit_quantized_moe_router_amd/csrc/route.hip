@@ -444,14 +444,22 @@ __global__ __launch_bounds__(256) void k_scatter(const int32_t* __restrict__ ids
 }
 
 // ------------------------------------------------------------------ launch
+int launch_router_logits(const moe_layer* L, const uint16_t* x, int T, moe_routing* R,
+                         void* stream) {
+  const int E = L->n_experts;
+  dim3 grid((E + 3) / 4, (T + 7) / 8);
+  hipLaunchKernelGGL(k_router_logits, grid, dim3(256), 0, (hipStream_t)stream, x, T, L->d, E,
+                     L->router_w, L->router_bias, R->logits);
+  return (int)hipGetLastError();
+}
+
 int launch_route_generic(const moe_layer* L, const uint16_t* x, int T, uint32_t flags,
                          moe_routing* R, uint8_t* ws, const PrefillWs& P, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  const int E = L->n_experts, k = L->top_k, d = L->d;
+  const int E = L->n_experts, k = L->top_k;
   if (!(flags & MOE_LOGITS_GIVEN)) {
-    dim3 grid((E + 3) / 4, (T + 7) / 8);
-    hipLaunchKernelGGL(k_router_logits, grid, dim3(256), 0, s, x, T, d, E, L->router_w,
-                       L->router_bias, R->logits);
+    const int rc = launch_router_logits(L, x, T, R, stream);
+    if (rc) return rc;
   }
 #define BQ_TK(PER)                                                                              \
   hipLaunchKernelGGL(k_topk<PER>, dim3((T + 3) / 4), dim3(256), 0, s, R->logits, T, E, k,      \

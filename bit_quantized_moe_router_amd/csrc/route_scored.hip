@@ -1,0 +1,575 @@
+// Routing by scores: softmax or sigmoid scores over all experts, a choice
+// value score + bias, a choice limited to the best groups of experts, the k
+// largest choice values, and the (renormalised, scaled) scores of the selected
+// experts as weights; then the same permutation as the other router's.
+//
+// The pages ("Xolotl" card, README "How it works, in one paragraph") give no
+// scoring function; the formulas are those of moe_scoring in include/moe.h.
+//
+// The selection is a comparison of values that lie arbitrarily close, so the
+// choice values are formed and compared in 64 bits: two experts with
+// different logits then keep their order unless they agree to about 1e-16,
+// which a 32-bit score (steps of 6e-8 below 1) would not give.  The vector
+// units run 64-bit multiply-adds at the rate of unpacked 32-bit ones, so this
+// costs little (an exponential per expert).
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "moe_internal.h"
+#include "topk_common.h"
+
+namespace bqmoe {
+
+// ------------------------------------------------------------- one token
+// Order-preserving 64-bit key of a choice value: NaN gets the lowest key of
+// all (1; key 0 marks "not in the choice"), -0 and +0 share one.
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  if (v != v) return 1ull;
+  if (v == 0.0) v = 0.0;  // -0 -> +0
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// The score of a logit: m and inv_sum are the row's maximum and 1 / sum of the
+// softmax (unused by the sigmoid).  A logit of -inf scores 0 in either.
+__device__ __forceinline__ double score_of(const ScoreArgs& S, float l, double m, double inv_sum) {
+  if (l == -INFINITY) return 0.0;
+  if (S.sigmoid) return 1.0 / (1.0 + exp(-(double)l));
+  return exp((double)l - m) * inv_sum;
+}
+
+// The two largest of (a1 >= a2) and (b1 >= b2), into a.
+__device__ __forceinline__ void merge_top2(uint64_t& a1, uint64_t& a2, uint64_t b1, uint64_t b2) {
+  const uint64_t lo = a1 < b1 ? a1 : b1;
+  const uint64_t second = a1 < b1 ? b2 : a2;
+  a1 = a1 < b1 ? b1 : a1;
+  a2 = lo > second ? lo : second;
+}
+
+// The value whose order_key64 is `key` (key 1, NaN's, gives a NaN).
+__device__ __forceinline__ double key_value64(uint64_t key) {
+  return __longlong_as_double((long long)((key >> 63) ? (key & 0x7FFFFFFFFFFFFFFFull) : ~key));
+}
+
+// One token by one wave (lane l holds experts l + 64 i): ids and weights of
+// the k selected experts in lanes 0..k-1.  `stage` is E keys of LDS of the
+// wave's own (read only where the choice is limited to groups).
+template <int PER>
+__device__ void wave_scored_topk(const ScoreArgs& S, const float* __restrict__ L, int lane,
+                                 uint64_t* stage, int& my_id, float& my_w) {
+  const int E = S.E, k = S.k;
+  float lg[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    lg[i] = e < E ? L[e] : -INFINITY;
+  }
+  double m = 0.0, inv_sum = 0.0;
+  if (!S.sigmoid) {
+    float mx = lg[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mx = fmaxf(mx, lg[i]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+    m = (double)mx;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lg[i] != -INFINITY) s += exp((double)lg[i] - m);
+    inv_sum = 1.0 / wave_sum64(s);
+  }
+  uint64_t key[PER];
+  int ix[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    ix[i] = e;
+    double c = score_of(S, lg[i], m, inv_sum);
+    if (S.bias) c += (double)S.bias[e < E ? e : 0];
+    if (lg[i] == -INFINITY) c = -INFINITY;  // a masked expert, whatever its bias
+    key[i] = e < E ? order_key64(c) : 0ull;
+  }
+  if (S.topk_groups < S.n_groups) {
+    // teams of 64 / 2^ceil(log2 groups) lanes find each group's largest choice values
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane + 64 * i < E) stage[lane + 64 * i] = key[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int ts = 1 << S.team_log2, g = lane >> S.team_log2, gs = S.group_size;
+    uint64_t a1 = 0, a2 = 0;
+    if (g < S.n_groups)
+      for (int i = lane & (ts - 1); i < gs; i += ts) merge_top2(a1, a2, stage[g * gs + i], 0ull);
+    for (int o = 1; o < ts; o <<= 1) {
+      const uint64_t b1 = __shfl_xor((unsigned long long)a1, o, 64);
+      const uint64_t b2 = __shfl_xor((unsigned long long)a2, o, 64);
+      merge_top2(a1, a2, b1, b2);
+    }
+    const uint64_t gv =
+        S.group_top == 1 ? a1 : order_key64(key_value64(a1) + key_value64(a2));
+    int better = 0;  // groups before this lane's: larger value, or equal and lower index
+    for (int h = 0; h < S.n_groups; ++h) {
+      const uint64_t o = __shfl((unsigned long long)gv, h << S.team_log2, 64);
+      better += (o > gv || (o == gv && h < g)) ? 1 : 0;
+    }
+    const uint64_t kept = __ballot(g < S.n_groups && better < S.topk_groups);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int ge = (int)(((uint32_t)ix[i] * S.group_magic) >> 20);  // ix / group_size
+      if (ix[i] < E && !((kept >> (ge << S.team_log2)) & 1)) key[i] = 0ull;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // each lane sorts its entries (larger key first, indices ascend with i)
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+#pragma unroll
+    for (int i = p & 1; i + 1 < PER; i += 2) {
+      const bool sw = key[i + 1] > key[i] || (key[i + 1] == key[i] && ix[i + 1] < ix[i]);
+      const uint64_t ka = key[i], kb = key[i + 1];
+      const int ia = ix[i], ib = ix[i + 1];
+      key[i] = sw ? kb : ka;
+      key[i + 1] = sw ? ka : kb;
+      ix[i] = sw ? ib : ia;
+      ix[i + 1] = sw ? ia : ib;
+    }
+  }
+  // k rounds: the largest head key, by its upper 32 bits first (one lane
+  // usually holds it alone), then its lower ones, then the lowest index
+  my_id = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t hi = (uint32_t)(key[0] >> 32), lo = (uint32_t)key[0];
+    uint64_t at = __ballot(hi == wave_allmax_u32(hi));
+    uint32_t win;
+    if (__popcll(at) > 1) {
+      const bool in = (at >> lane) & 1;
+      const uint32_t lmax = wave_allmax_u32(in ? lo : 0u);
+      win = ~wave_allmax_u32(in && lo == lmax ? ~(uint32_t)ix[0] : 0u);
+    } else {
+      win = (uint32_t)__builtin_amdgcn_readlane(ix[0], (int)__ffsll((unsigned long long)at) - 1);
+    }
+    const bool pop = (uint32_t)ix[0] == win;
+#pragma unroll
+    for (int t = 0; t + 1 < PER; ++t) {
+      key[t] = pop ? key[t + 1] : key[t];
+      ix[t] = pop ? ix[t + 1] : ix[t];
+    }
+    key[PER - 1] = pop ? 0ull : key[PER - 1];
+    my_id = lane == j ? (int)win : my_id;
+  }
+  // weights from the scores, without the bias
+  double s = lane < k ? score_of(S, L[my_id], m, inv_sum) : 0.0;
+  if (S.renorm) {
+    const double den = wave_sum64(s);
+    s = den == 0.0 ? 0.0 : s / den;
+  }
+  my_w = (float)(s * (double)S.scale);
+}
+
+// Lanes whose `key` (< 2^bits) equals this lane's, among `active` lanes.
+__device__ __forceinline__ uint64_t match_lanes(int key, int bits, uint64_t active) {
+  uint64_t peers = active;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t m = __ballot((key >> b) & 1);
+    peers &= ((key >> b) & 1) ? m : ~m;
+  }
+  return peers;
+}
+
+// Exclusive scan of one value per thread over the block; `tot` holds one int
+// per wave and one more (the total, on return in every thread through `all`).
+__device__ __forceinline__ int block_scan(int v, int* tot, int& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 63) tot[wave] = incl;
+  __syncthreads();
+  int before = 0, sum = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int t = tot[w];
+    before += w < wave ? t : 0;
+    sum += t;
+  }
+  __syncthreads();
+  all = sum;
+  return before + incl - v;
+}
+
+// The grouped-GEMM tile list (routed experts in id order, then the shared
+// expert) from expert tid's row count and offset; every thread of a block of
+// at least E calls it.
+__device__ __forceinline__ void write_tiles(const ScoreOut& O, int T, int k, int E, int count,
+                                            int off, int* tot) {
+  const int n = (count + O.tm - 1) / O.tm;
+  int ntiles;
+  const int first = block_scan(n, tot, ntiles);
+  for (int i = 0; i < n; ++i) {
+    int32_t* t = O.tiles + 4 * (first + i);
+    t[0] = threadIdx.x;
+    t[1] = off + i * O.tm;
+    t[2] = min(O.tm, count - i * O.tm);
+    t[3] = 0;
+  }
+  const int nsh = O.n_shared ? (T + O.tm - 1) / O.tm : 0;
+  for (int i = threadIdx.x; i < nsh; i += blockDim.x) {
+    int32_t* t = O.tiles + 4 * (ntiles + i);
+    t[0] = -1;
+    t[1] = T * k + i * O.tm;
+    t[2] = min(O.tm, T - i * O.tm);
+    t[3] = 0;
+  }
+  if (threadIdx.x == 0) O.ctrl[0] = ntiles + nsh;
+}
+
+// ------------------------------------------------------------ few tokens
+// One block does everything for at most 1024 rows: the waves take the tokens
+// in turn, then the rows sit 64 to a wave, each wave ranks its rows among
+// themselves by ballots over the expert id's bits, and thread e sums the
+// waves' counts of expert e and scans them over the experts.  cnt is
+// [chunks][E] in LDS.
+template <int PER, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float* __restrict__ logits,
+                                                        int T, ScoreOut O) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+  __shared__ int s_row[kScoredFewRows];
+  __shared__ int s_tot[THREADS / 64];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int E = S.E, k = S.k, rows = T * k;
+  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * E;
+  for (int t = wave; t < T; t += THREADS / 64) {
+    int id;
+    float w;
+    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, id, w);
+    if (lane < k) {
+      O.ids[t * k + lane] = id;
+      O.w[t * k + lane] = w;
+      s_row[t * k + lane] = id;
+    }
+  }
+  __syncthreads();
+  const int chunks = (rows + 63) >> 6;
+  int* cnt = reinterpret_cast<int*>(sm);
+  for (int i = tid; i < chunks * E; i += THREADS) cnt[i] = 0;
+  __syncthreads();
+  // row r = tid (+ THREADS): its rank among the rows of the same expert in its chunk
+  constexpr int RP = kScoredFewRows / THREADS;
+  int rk[RP];
+#pragma unroll
+  for (int q = 0; q < RP; ++q) {
+    const int r = q * THREADS + tid;
+    const bool act = r < rows;
+    const uint64_t active = __ballot(act);
+    if (active) {
+      const int e = act ? s_row[r] : 0;
+      const uint64_t peers = match_lanes(e, S.bits, active);
+      const uint64_t lt = lane ? (~0ull >> (64 - lane)) : 0ull;
+      rk[q] = __popcll(peers & lt);
+      if (act && (peers & lt) == 0) cnt[(r >> 6) * E + e] = __popcll(peers);
+    }
+  }
+  __syncthreads();
+  // thread e: counts before each chunk, the expert's total; then offset and slot
+  int total = 0;
+  if (tid < E)
+    for (int c = 0; c < chunks; ++c) {
+      const int v = cnt[c * E + tid];
+      cnt[c * E + tid] = total;
+      total += v;
+    }
+  int all;
+  const int ex = block_scan(total | (total ? 1 << 16 : 0), s_tot, all);  // rows <= 1024 < 2^16
+  const int off = ex & 0xFFFF, slot = ex >> 16;
+  const int n_active = all >> 16;
+  if (tid < E) {
+    O.counts[tid] = total;
+    O.offsets[tid] = off;
+    for (int c = 0; c < chunks; ++c) cnt[c * E + tid] += off;
+    if (O.slots && total) {
+      int32_t* rec = O.slots + kSlotRec * (1 + slot);
+      rec[0] = tid;
+      rec[1] = off;
+      rec[2] = total;
+      rec[3] = O.alt_select && O.alt_select[tid] ? 1 : 0;
+      // the tokens of the slot's rows, in ascending order (T <= 8 with slots)
+      int n = 0;
+      for (int r = 0; r < rows; ++r)
+        if (s_row[r] == tid) rec[kSlotTok + n++] = r / k;
+    }
+  }
+  if (tid == 0) O.offsets[E] = rows;
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < RP; ++q) {
+    const int r = q * THREADS + tid;
+    if (r < rows) {
+      const int pos = cnt[(r >> 6) * E + s_row[r]] + rk[q];
+      O.perm_tok[pos] = r / k;
+      O.inv_row[r] = pos;
+    }
+  }
+  if (O.slots) {
+    const int n_slots = n_active + (O.n_shared ? 1 : 0);
+    if (tid == 0) O.slots[0] = n_slots;
+    if (O.n_shared && tid < T) {
+      int32_t* rec = O.slots + kSlotRec * (1 + n_active);
+      if (tid == 0) {
+        rec[0] = -1;
+        rec[1] = rows;
+        rec[2] = T;
+        rec[3] = 0;
+      }
+      rec[kSlotTok + tid] = tid;
+    }
+    for (int s = n_slots + tid; s < O.max_slots; s += THREADS)
+      for (int j = 0; j < kSlotTok; ++j) O.slots[kSlotRec * (1 + s) + j] = 0;
+  }
+  if (O.tiles) write_tiles(O, T, k, E, tid < E ? total : 0, off, s_tot);
+}
+
+// ----------------------------------------------------------- many tokens
+// Block b: tokens [b * tb, (b + 1) * tb).  The waves select, then rank the
+// block's rows per expert (64-row chunks, contiguous ones to a wave, by
+// ballots), giving each row its rank among the block's rows of its expert and
+// the block's histogram.
+template <int PER, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
+                                                           const float* __restrict__ logits, int T,
+                                                           int tb, int32_t* __restrict__ ids,
+                                                           float* __restrict__ w,
+                                                           int32_t* __restrict__ hist,
+                                                           int32_t* __restrict__ lrank) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+  constexpr int NW = THREADS / 64;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int E = S.E, k = S.k;
+  const int t0 = blockIdx.x * tb, t1 = min(T, t0 + tb);
+  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * E;
+  int* s_row = reinterpret_cast<int*>(sm + (size_t)NW * E * 8);
+  for (int t = t0 + wave; t < t1; t += NW) {
+    int id;
+    float wt;
+    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, id, wt);
+    if (lane < k) {
+      ids[(size_t)t * k + lane] = id;
+      w[(size_t)t * k + lane] = wt;
+      s_row[(t - t0) * k + lane] = id;
+    }
+  }
+  __syncthreads();
+  int* cnt = reinterpret_cast<int*>(sm);  // [NW][E], over the staging area
+  for (int i = tid; i < NW * E; i += THREADS) cnt[i] = 0;
+  __syncthreads();
+  const int nrows = (t1 - t0) * k;
+  const int nchunk = (nrows + 63) >> 6, per = (nchunk + NW - 1) / NW;
+  const int c0 = wave * per, c1 = min(nchunk, c0 + per);
+  const size_t r0 = (size_t)t0 * k;
+  for (int c = c0; c < c1; ++c) {
+    const int r = c * 64 + lane;
+    const bool act = r < nrows;
+    const int e = act ? s_row[r] : 0;
+    const uint64_t peers = match_lanes(e, S.bits, __ballot(act));
+    const uint64_t lt = lane ? (~0ull >> (64 - lane)) : 0ull;
+    // a wave's LDS accesses complete in program order: all lanes read, then
+    // the first lane of each expert writes
+    const int base = act ? cnt[wave * E + e] : 0;
+    if (act) lrank[r0 + r] = base + __popcll(peers & lt);
+    if (act && (peers & lt) == 0) cnt[wave * E + e] = base + __popcll(peers);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += THREADS) {
+    int run = 0;
+    for (int v = 0; v < NW; ++v) {
+      const int c = cnt[v * E + e];
+      cnt[v * E + e] = run;
+      run += c;
+    }
+    hist[(size_t)blockIdx.x * E + e] = run;
+  }
+  __syncthreads();
+  for (int c = c0; c < c1; ++c) {
+    const int r = c * 64 + lane;
+    if (r < nrows) lrank[r0 + r] += cnt[wave * E + s_row[r]];
+  }
+}
+
+// Block b places the rows of the select blocks [b * sb, (b + 1) * sb).  Each
+// block sums the histogram's columns itself (all of it for the offsets, the
+// blocks before its own for its first base): nblk * E integers from L2, less
+// than a launch in between would cost.
+__global__ __launch_bounds__(1024) void k_scored_place(const int32_t* __restrict__ ids, int T, int E,
+                                                       int k, int tb, int sb, int nblk,
+                                                       const int32_t* __restrict__ hist,
+                                                       const int32_t* __restrict__ lrank,
+                                                       ScoreOut O) {
+  __shared__ int s_all[MOE_MAX_EXPERTS], s_base[MOE_MAX_EXPERTS];
+  __shared__ int s_tot[16];
+  const int tid = threadIdx.x;
+  const int b0 = blockIdx.x * sb, b1 = min(nblk, b0 + sb);
+  s_all[tid] = 0;
+  s_base[tid] = 0;
+  __syncthreads();
+  // thread = (expert, one of `parts` interleaved sets of select blocks); integer sums only
+  const int parts = max(1, 1024 / E), part = tid / E, e = tid - part * E;
+  if (part < parts) {
+    int all = 0, base = 0;
+#pragma unroll 8
+    for (int b = part; b < nblk; b += parts) {
+      const int v = hist[(size_t)b * E + e];
+      all += v;
+      base += b < b0 ? v : 0;
+    }
+    atomicAdd(&s_all[e], all);
+    atomicAdd(&s_base[e], base);
+  }
+  __syncthreads();
+  const int total = tid < E ? s_all[tid] : 0;
+  int sum;
+  const int off = block_scan(total, s_tot, sum);
+  if (tid < E) s_base[tid] += off;
+  if (blockIdx.x == 0) {
+    if (tid < E) {
+      O.counts[tid] = total;
+      O.offsets[tid] = off;
+    }
+    if (tid == 0) O.offsets[E] = sum;
+    if (O.tiles) write_tiles(O, T, k, E, total, off, s_tot);
+  }
+  for (int b = b0; b < b1; ++b) {
+    __syncthreads();
+    const int r0 = b * tb * k, r1 = min(T * k, r0 + tb * k);
+    for (int r = r0 + tid; r < r1; r += 1024) {
+      const int pos = s_base[ids[r]] + lrank[r];
+      O.perm_tok[pos] = r / k;
+      O.inv_row[r] = pos;
+    }
+    __syncthreads();
+    if (tid < E) s_base[tid] += hist[(size_t)b * E + tid];
+  }
+}
+
+// ------------------------------------------------------------------ launch
+static int bits_for(int n) {
+  int b = 1;
+  while ((1 << b) < n) ++b;
+  return b;
+}
+
+// tokens per select block: about 256 blocks (one per CU), at least one token
+// a wave, and at most 8192 rows (32 KB of LDS)
+static int scored_block_tokens(int T, int k, int waves) {
+  const int per = (T + 255) / 256, most = 8192 / k / waves * waves;
+  const int tb = (per + waves - 1) / waves * waves;
+  return tb < most ? tb : most;
+}
+static int scored_waves(int E) { return E <= 256 ? 16 : 8; }
+
+size_t scored_ws_bytes(const moe_layer* L, int T) {
+  const int tb = scored_block_tokens(T, L->top_k, scored_waves(L->n_experts));
+  const size_t nblk = ((size_t)T + tb - 1) / tb;
+  return 4 * (nblk * (size_t)L->n_experts + (size_t)T * L->top_k) + 256;
+}
+
+int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_routing* R,
+                        uint8_t* scratch, const ScoreOut& out, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  const int E = L->n_experts, k = L->top_k;
+  ScoreArgs S{};
+  S.bias = C->choice_bias;
+  S.scale = C->scale;
+  S.E = E;
+  S.k = k;
+  S.sigmoid = C->score == MOE_SCORE_SIGMOID;
+  S.renorm = C->renorm;
+  S.n_groups = C->n_groups;
+  S.topk_groups = C->topk_groups;
+  S.group_top = C->group_top;
+  S.group_size = E / C->n_groups;
+  S.group_magic = ((1u << 20) + S.group_size - 1) / S.group_size;
+  S.team_log2 = 6 - (C->n_groups > 1 ? bits_for(C->n_groups) : 0);
+  S.bits = bits_for(E);
+  const bool grouped = S.topk_groups < S.n_groups;
+  ScoreOut O = out;
+  O.ids = R->topk_ids;
+  O.w = R->topk_w;
+  O.counts = R->counts;
+  O.offsets = R->offsets;
+  O.perm_tok = R->perm_tok;
+  O.inv_row = R->inv_row;
+  const int rows = T * k;
+  if (T <= kScoredFewTokens && rows <= kScoredFewRows) {
+    const int threads = E <= 256 && T <= 4 && rows <= 256 ? 256 : 1024;
+    const size_t cnt = (size_t)((rows + 63) / 64) * E * 4;
+    const size_t stg = grouped ? (size_t)(threads / 64) * E * 8 : 0;
+    const size_t lds = cnt > stg ? cnt : stg;
+#define BQ_FEW(PER, TH)                                                                       \
+  do {                                                                                        \
+    const void* f = (const void*)k_scored_few<PER, TH>;                                       \
+    if (lds > 65536 - 8192 &&                                                                 \
+        hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=       \
+            hipSuccess)                                                                       \
+      return (int)hipErrorInvalidConfiguration;                                               \
+    hipLaunchKernelGGL((k_scored_few<PER, TH>), dim3(1), dim3(TH), lds, s, S, R->logits, T, O); \
+  } while (0)
+    if (threads == 256) {
+      if (E <= 64)
+        BQ_FEW(1, 256);
+      else if (E <= 128)
+        BQ_FEW(2, 256);
+      else
+        BQ_FEW(4, 256);
+    } else if (E <= 64)
+      BQ_FEW(1, 1024);
+    else if (E <= 128)
+      BQ_FEW(2, 1024);
+    else if (E <= 256)
+      BQ_FEW(4, 1024);
+    else if (E <= 512)
+      BQ_FEW(8, 1024);
+    else
+      BQ_FEW(16, 1024);
+#undef BQ_FEW
+    return (int)hipGetLastError();
+  }
+  const int waves = scored_waves(E), tb = scored_block_tokens(T, k, waves);
+  const int nblk = (T + tb - 1) / tb;
+  int32_t* hist = (int32_t*)scratch;
+  int32_t* lrank = hist + (size_t)nblk * E;
+  const size_t lds = (size_t)waves * E * 8 + (size_t)tb * k * 4;
+#define BQ_SEL(PER, TH)                                                                        \
+  do {                                                                                         \
+    const void* f = (const void*)k_scored_select<PER, TH>;                                     \
+    if (lds > 65536 &&                                                                         \
+        hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) !=        \
+            hipSuccess)                                                                        \
+      return (int)hipErrorInvalidConfiguration;                                                \
+    hipLaunchKernelGGL((k_scored_select<PER, TH>), dim3(nblk), dim3(TH), lds, s, S, R->logits, \
+                       T, tb, R->topk_ids, R->topk_w, hist, lrank);                            \
+  } while (0)
+  if (E <= 64)
+    BQ_SEL(1, 1024);
+  else if (E <= 128)
+    BQ_SEL(2, 1024);
+  else if (E <= 256)
+    BQ_SEL(4, 1024);
+  else if (E <= 512)
+    BQ_SEL(8, 512);
+  else
+    BQ_SEL(16, 512);
+#undef BQ_SEL
+  const int sb = (nblk + 63) / 64;
+  hipLaunchKernelGGL(k_scored_place, dim3((nblk + sb - 1) / sb), dim3(1024), 0, s, R->topk_ids, T,
+                     E, k, tb, sb, nblk, hist, lrank, O);
+  return (int)hipGetLastError();
+}
+
+}  // namespace bqmoe

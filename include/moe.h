@@ -194,7 +194,7 @@ typedef struct {           /* caller-allocated device buffers, written by the ca
 } moe_routing;
 
 /* Device workspace needed by moe_route_topk / moe_forward_decode /
- * moe_forward_prefill for T tokens (the largest of the three).  0 if the
+ * moe_forward_prefill and their _scored forms for T tokens (the largest).  0 if the
  * layer description is invalid. */
 size_t moe_workspace_bytes(const moe_layer* L, int32_t T);
 
@@ -273,6 +273,58 @@ moe_status moe_forward_decode_stages(const moe_layer* L, const uint16_t* x, int3
 moe_status moe_forward_prefill_stages(const moe_layer* L, const uint16_t* x, int32_t T,
                                       uint32_t flags, moe_routing* R, void* ws, size_t ws_bytes,
                                       uint16_t* out, uint32_t stage_mask, void* stream);
+
+/* -------------------------------------------------------- routing by scores
+ * Another router for the same layer: every expert gets a score, a bias may
+ * steer the choice without touching the weights (balance between experts),
+ * and the choice may be limited to the best groups of experts.  The pages
+ * name an additive route bias ("Xolotl" card, README "What one PC can do",
+ * --route-bias) but give no formula; the definition is this library's.  For
+ * each token, from its E logits l:
+ *   score:  softmax  s_e = exp(l_e - max l) / sum_i exp(l_i - max l)
+ *           sigmoid  s_e = 1 / (1 + exp(-l_e))
+ *   choice: c_e = s_e + choice_bias[e];  c_e = -inf where l_e = -inf
+ *   groups: the E experts are n_groups runs of E / n_groups; a group's value
+ *           is the sum of its group_top largest c, and only the topk_groups
+ *           groups of largest value (the lower group first on ties) are in
+ *   ids:    the top_k largest c of those groups, descending, the lower index
+ *           first on ties
+ *   w_j  =  scale * s[ids_j] [ / sum_i s[ids_i] if renorm ]
+ * Scores, sums and choice values are 64-bit, w is rounded to fp32 once.
+ * A logit of -inf takes its expert out: score 0, chosen only when fewer than
+ * top_k others are in (then with weight 0).  A row of nothing but -inf gets
+ * weights 0; so does a renormalised row whose selected scores sum to 0.  A
+ * NaN choice value ranks below -inf; a NaN or +inf logit makes all softmax
+ * scores of its row NaN (the ids are still distinct and in range).
+ * With softmax, renorm, scale 1, no bias and no groups this is the layer's
+ * own router. */
+typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score;
+enum { MOE_MAX_GROUPS = 64 };
+typedef struct {
+  int32_t score;            /* moe_score */
+  int32_t n_groups;         /* 1..64, divides n_experts; 1 = no groups */
+  int32_t topk_groups;      /* 1..n_groups; topk_groups * (E / n_groups) >= top_k */
+  int32_t group_top;        /* 1 or 2 (at most E / n_groups) */
+  int32_t renorm;           /* 0 or 1 */
+  float scale;              /* finite */
+  const float* choice_bias; /* device fp32 [E], or NULL */
+} moe_scoring;
+
+/* moe_route_topk with the router S: the same arguments, checks and outputs
+ * (also MOE_ERR_INVALID_ARG for a moe_scoring outside the ranges above).
+ * ws_bytes >= moe_workspace_bytes(L, T). */
+moe_status moe_route_scored(const moe_layer* L, const moe_scoring* S, const uint16_t* x,
+                            int32_t T, uint32_t flags, moe_routing* R, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* moe_forward_decode and moe_forward_prefill with the router S: the same
+ * arguments, limits, checks and expert products. */
+moe_status moe_forward_decode_scored(const moe_layer* L, const moe_scoring* S, const uint16_t* x,
+                                     int32_t T, uint32_t flags, moe_routing* R, void* ws,
+                                     size_t ws_bytes, uint16_t* out, void* stream);
+moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_scoring* S, const uint16_t* x,
+                                      int32_t T, uint32_t flags, moe_routing* R, void* ws,
+                                      size_t ws_bytes, uint16_t* out, void* stream);
 
 /* ---------------------------------------------------------- no allocation
  * For callers that cannot allocate device memory (code under HIP graph
