@@ -25,6 +25,9 @@ MOE_LOGITS_GIVEN, MOE_ADD_RESIDUAL = 1, 2
 MOE_MAX_DECODE_TOKENS = 8
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 1, 2
 MOE_MAX_GROUPS = 64
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_RELU2, \
+    MOE_ACT_SIGMOID = range(7)
+MOE_MAX_LINEAR_ROWS = 1 << 24
 MOE_DECODE_STAGE_ROUTE, MOE_DECODE_STAGE_SELECT, MOE_DECODE_STAGE_GATEUP, MOE_DECODE_STAGE_DOWN = \
     1, 2, 4, 8
 MOE_DECODE_STAGES_ALL = 15
@@ -38,6 +41,7 @@ EXPORTED = ("moe_packed_bytes", "moe_expert_bytes", "moe_pack_weights", "moe_qua
             "moe_route_topk", "moe_forward_decode", "moe_forward_prefill",
             "moe_forward_decode_stages", "moe_forward_prefill_stages",
             "moe_route_scored", "moe_forward_decode_scored", "moe_forward_prefill_scored",
+            "moe_linear_workspace_bytes", "moe_linear_forward",
             "moe_forward_decode_noalloc", "moe_status_string", "moe_abi_version")
 
 
@@ -72,6 +76,11 @@ class moe_scoring(ctypes.Structure):
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
                 ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("choice_bias", ctypes.c_void_p)]
+
+
+class moe_linear(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("qtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -110,7 +119,12 @@ def load():
     lib.moe_route_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp]
     lib.moe_forward_decode_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp, vp]
     lib.moe_forward_prefill_scored.argtypes = [L, S, vp, ctypes.c_int32, u32, R, vp, sz, vp, vp]
-    for f in (lib.moe_route_scored, lib.moe_forward_decode_scored, lib.moe_forward_prefill_scored,
+    P = ctypes.POINTER(moe_linear)
+    lib.moe_linear_workspace_bytes.argtypes = [P, ctypes.c_int32]
+    lib.moe_linear_workspace_bytes.restype = sz
+    lib.moe_linear_forward.argtypes = [P, vp, i64, ctypes.c_int32, vp, i64, vp, i64, vp, i64, vp,
+                                       sz, vp]
+    for f in (lib.moe_linear_forward, lib.moe_route_scored, lib.moe_forward_decode_scored, lib.moe_forward_prefill_scored,
               lib.moe_route_topk, lib.moe_forward_decode, lib.moe_forward_prefill,
               lib.moe_forward_decode_stages, lib.moe_forward_prefill_stages,
               lib.moe_forward_decode_noalloc):
@@ -349,6 +363,70 @@ def moe_forward_prefill_scored(layer: Layer, scoring: Scoring, x, T: int, flags:
                                            0 if ws is None else ws.numel(), _ptr(out),
                                            _stream(stream))
     _check(st, "moe_forward_prefill_scored")
+
+
+# ------------------------------------------------------ dense product
+@dataclass
+class Linear:
+    """A moe_linear plus the tensors it points into (kept alive here)."""
+    c: moe_linear
+    tensors: tuple
+
+
+def make_linear(K: int, N: int, qtype: int, w, bias=None, act: int = MOE_ACT_NONE) -> Linear:
+    """w: the packed projection (moe_pack_weights) in device memory; bias: device fp32 [N]."""
+    if isinstance(bias, torch.Tensor) and (bias.dtype != torch.float32
+                                           or not bias.is_contiguous() or bias.numel() != N):
+        raise MoeError(MOE_ERR_INVALID_ARG, "make_linear: bias must be N contiguous float32")
+    if isinstance(w, torch.Tensor) and (not w.is_contiguous() or w.numel() * w.element_size()
+                                        < moe_packed_bytes(qtype, K, N)):
+        raise MoeError(MOE_ERR_INVALID_ARG, "make_linear: w is not the packed projection")
+    return Linear(moe_linear(K, N, qtype, act, _ptr(w), _ptr(bias)), (w, bias))
+
+
+def moe_linear_workspace_bytes(linear: Linear, T: int) -> int:
+    return int(load().moe_linear_workspace_bytes(ctypes.byref(linear.c), T))
+
+
+def alloc_linear_workspace(linear: Linear, T: int, device="cuda") -> torch.Tensor:
+    n = moe_linear_workspace_bytes(linear, T)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_linear_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _rows(t, width: int, T: int, device, what: str):
+    """(address, row stride) of a [T][width] operand of 16-bit values on `device`."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.element_size() != 2 or t.shape[0] < T or t.shape[1] != width or \
+            (t.stride(1) != 1 and width > 1) or t.device != device or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"moe_linear_forward: {what} must be at least {T} rows "
+                       f"of {width} adjacent 16-bit values on {device}")
+    return t.data_ptr(), t.stride(0) if T > 1 else -(-width // 8) * 8
+
+
+def moe_linear_forward(linear: Linear, x: torch.Tensor, T: int, out: torch.Tensor,
+                       ws: torch.Tensor | None, mul: torch.Tensor | None = None,
+                       residual: torch.Tensor | None = None, stream=None):
+    """out = bf16([residual +] [mul *] act(x.W + bias)) over the first T rows of the 2-d device
+    tensors x [.][K], mul, residual and out [.][N] (bf16 values or their bit patterns; rows may be
+    any multiple of 8 values apart).  Runs on x's device, on its current stream by default."""
+    c, dev = linear.c, x.device
+    if x.is_cuda and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return moe_linear_forward(linear, x, T, out, ws, mul, residual, stream)
+    xp, xs = _rows(x, c.K, T, dev, "x")
+    mp, ms = _rows(mul, c.N, T, dev, "mul")
+    rp, rs = _rows(residual, c.N, T, dev, "residual")
+    op, os_ = _rows(out, c.N, T, dev, "out")
+    for t in (*linear.tensors, ws):
+        if isinstance(t, torch.Tensor) and t.device != dev:
+            raise MoeError(MOE_ERR_INVALID_ARG, f"moe_linear_forward: a tensor is not on {dev}")
+    st = load().moe_linear_forward(ctypes.byref(c), xp, xs, T, mp, ms, rp, rs, op, os_, _ptr(ws),
+                                   0 if ws is None else ws.numel() * ws.element_size(),
+                                   _stream(stream))
+    _check(st, "moe_linear_forward")
 
 
 def moe_abi_version() -> int:

@@ -346,6 +346,64 @@ extern "C" moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_s
              : MOE_OK;
 }
 
+// ----------------------------------------------------------- dense product
+namespace bqmoe {
+static bool linear_ok(const moe_linear* P) {
+  return P && P->K > 0 && P->N > 0 && P->act >= MOE_ACT_NONE && P->act <= MOE_ACT_SIGMOID;
+}
+static bool linear_supported(const moe_linear* P) {
+  return P->K <= MOE_MAX_DIM && P->N <= MOE_MAX_DIM && format_shape_ok(P->qtype, P->K, P->N);
+}
+// a [T][width] operand of 16-byte aligned rows
+static bool rows_ok(const void* p, int64_t ld, int64_t width) {
+  return aligned(p, 16) && ld >= width && ld % 8 == 0 && ld <= (int64_t)1 << 40;
+}
+static size_t rows_bytes(int32_t T, int64_t ld, int64_t width) {
+  return ((size_t)(T - 1) * (size_t)ld + (size_t)width) * 2;
+}
+}  // namespace bqmoe
+
+extern "C" size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T) {
+  if (!linear_ok(P) || !linear_supported(P) || T < 0) return 0;
+  return lin_ws_layout(P->K, P->N, T).total;
+}
+
+extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x, int64_t x_stride,
+                                         int32_t T, const uint16_t* mul, int64_t mul_stride,
+                                         const uint16_t* residual, int64_t residual_stride,
+                                         uint16_t* out, int64_t out_stride, void* ws,
+                                         size_t ws_bytes, void* stream) {
+  if (!linear_ok(P)) return MOE_ERR_INVALID_ARG;
+  if (!linear_supported(P)) return MOE_ERR_UNSUPPORTED;
+  if (T < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (T > MOE_MAX_LINEAR_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (!P->w || !aligned(P->w, 256) || !aligned(P->bias, 4)) return MOE_ERR_INVALID_ARG;
+  if (!x || !rows_ok(x, x_stride, P->K)) return MOE_ERR_INVALID_ARG;
+  if (mul && !rows_ok(mul, mul_stride, P->N)) return MOE_ERR_INVALID_ARG;
+  if (residual && !rows_ok(residual, residual_stride, P->N)) return MOE_ERR_INVALID_ARG;
+  if (!out || !rows_ok(out, out_stride, P->N)) return MOE_ERR_INVALID_ARG;
+  // out may be mul or residual itself (each value is read before it is
+  // written, by the same thread), but not x, nor either of them shifted
+  const size_t ob = rows_bytes(T, out_stride, P->N);
+  if (overlaps(x, rows_bytes(T, x_stride, P->K), out, ob)) return MOE_ERR_INVALID_ARG;
+  if (mul && !(mul == out && mul_stride == out_stride) &&
+      overlaps(mul, rows_bytes(T, mul_stride, P->N), out, ob))
+    return MOE_ERR_INVALID_ARG;
+  if (residual && !(residual == out && residual_stride == out_stride) &&
+      overlaps(residual, rows_bytes(T, residual_stride, P->N), out, ob))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = lin_ws_layout(P->K, P->N, T).total;
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!aligned(ws, 256) || overlaps(ws, need, out, ob)) return MOE_ERR_INVALID_ARG;
+  const PackedLayout pl = packed_layout(P->qtype, P->K, P->N);
+  const LinArgs A = {(const uint8_t*)P->w, pl.plane1, pl.scales, P->bias,  x,
+                     mul,                  residual,  out,       x_stride, mul_stride,
+                     residual_stride,      out_stride, P->K,     P->N,     P->qtype,
+                     P->act};
+  return launch_linear(A, T, (uint8_t*)ws, stream) ? MOE_ERR_DEVICE : MOE_OK;
+}
+
 extern "C" const char* moe_status_string(moe_status s) {
   switch (s) {
     case MOE_OK: return "ok";

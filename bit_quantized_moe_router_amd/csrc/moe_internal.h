@@ -118,6 +118,25 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
 int launch_decode_route(const moe_layer* L, const uint16_t* x, int T, uint32_t flags,
                         moe_routing* R, uint8_t* ws, const DecodeWs& W, void* stream,
                         uint32_t mask);
+// Dense product with packed weights: the call's operands as the kernels take them.
+struct LinArgs {
+  const uint8_t* w;       // packed projection
+  uint64_t plane1, scales;  // byte offsets in it
+  const float* bias;
+  const uint16_t *x, *mul, *res;
+  uint16_t* out;
+  int64_t ldx, ldm, ldr, ldo;  // row strides in values
+  int32_t K, N, q, act;
+};
+struct LinWs {
+  size_t xs;      // fp16 [T][K]  x * 2^-e
+  size_t rscale;  // fp32 [T]     2^e
+  size_t cscale;  // fp32 [N]     2^-f
+  size_t total;
+};
+constexpr int kLinFewRows = 64;  // rows up to which the bandwidth kernel runs
+LinWs lin_ws_layout(int K, int N, int T);
+int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream);
 // Whether the decode kernels take this layer for T tokens (LDS and register
 // limits of their launch shapes).
 bool decode_shape_ok(const moe_layer* L, int T);

@@ -326,6 +326,58 @@ moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_scoring* S, 
                                       int32_t T, uint32_t flags, moe_routing* R, void* ws,
                                       size_t ws_bytes, uint16_t* out, void* stream);
 
+/* ------------------------------------------------------------ dense product
+ * The projections of a model that are no experts (attention output, dense
+ * feed-forward layers, the two halves of a gated one) with weights in the same
+ * packed format, and what follows them in the same pass:
+ *
+ *   out[t][n] = bf16( [residual[t][n] +] [mul[t][n] *]
+ *                     act( sum_k x[t][k] * W[k][n] [+ bias[n]] ) )
+ *
+ * Sums, bias, activation, product and residual are fp32, rounded to bf16
+ * once.  For up to 64 rows the weights enter the product exactly; beyond,
+ * 2- and 3-bit weights s * (u - offset) are rounded to fp16's 11 significant
+ * bits (at most 2^-12 of a weight; ternary ones are exact), and values of x
+ * below 2^-31 of their row's largest may lose bits.
+ * The pages name the weights' code families only; the call is this library's. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,      /* v * sigmoid(v) */
+  MOE_ACT_GELU = 2,      /* v * (1 + erf(v / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 3, /* v * (1 + tanh(sqrt(2/pi) * (v + 0.044715 v^3))) / 2 */
+  MOE_ACT_RELU = 4,
+  MOE_ACT_RELU2 = 5,     /* relu(v)^2 */
+  MOE_ACT_SIGMOID = 6
+} moe_act;
+enum { MOE_MAX_LINEAR_ROWS = 1 << 24 };
+typedef struct {
+  int32_t K, N;      /* K % 128 == 0, N % 16 == 0, both up to MOE_MAX_DIM */
+  int32_t qtype;     /* moe_qtype of w */
+  int32_t act;       /* moe_act */
+  const void* w;     /* device: the packed projection (moe_pack_weights), 256-B aligned */
+  const float* bias; /* device fp32 [N], or NULL */
+} moe_linear;
+
+/* Device workspace of moe_linear_forward for T rows (0 if the description is invalid). */
+size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T);
+
+/*   x        : device bf16 [T][K], rows x_stride values apart
+ *   mul      : device bf16 [T][N], rows mul_stride apart, or NULL
+ *   residual : device bf16 [T][N], rows residual_stride apart, or NULL
+ *   out      : device bf16 [T][N], rows out_stride apart; it may be mul or
+ *              residual itself (same address and stride), and overlaps nothing
+ *              else.  Only the N values of its T rows are written.
+ *   ws       : device workspace of ws_bytes >= moe_linear_workspace_bytes(P, T)
+ * Rows start at 16-byte aligned addresses: pointers are 16-byte aligned and
+ * strides multiples of 8, at least the row's length.
+ * Errors: MOE_ERR_UNSUPPORTED for a shape or family outside the packed format
+ * or the limits above, MOE_ERR_WORKSPACE for a missing or short workspace,
+ * MOE_ERR_INVALID_ARG otherwise. */
+moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x, int64_t x_stride, int32_t T,
+                              const uint16_t* mul, int64_t mul_stride, const uint16_t* residual,
+                              int64_t residual_stride, uint16_t* out, int64_t out_stride, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------- no allocation
  * For callers that cannot allocate device memory (code under HIP graph
  * capture, serving loops and harnesses that forbid hipMalloc): the same layer
