@@ -354,9 +354,10 @@ static bool linear_ok(const moe_linear* P) {
 static bool linear_supported(const moe_linear* P) {
   return P->K <= MOE_MAX_DIM && P->N <= MOE_MAX_DIM && format_shape_ok(P->qtype, P->K, P->N);
 }
+constexpr int64_t kLinMaxStride = MOE_MAX_LINEAR_STRIDE;
 // a [T][width] operand of 16-byte aligned rows
 static bool rows_ok(const void* p, int64_t ld, int64_t width) {
-  return aligned(p, 16) && ld >= width && ld % 8 == 0 && ld <= (int64_t)1 << 40;
+  return aligned(p, 16) && ld >= width && ld % 8 == 0;
 }
 static size_t rows_bytes(int32_t T, int64_t ld, int64_t width) {
   return ((size_t)(T - 1) * (size_t)ld + (size_t)width) * 2;
@@ -365,7 +366,7 @@ static size_t rows_bytes(int32_t T, int64_t ld, int64_t width) {
 
 extern "C" size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T) {
   if (!linear_ok(P) || !linear_supported(P) || T < 0) return 0;
-  return lin_ws_layout(P->K, P->N, T).total;
+  return lin_ws_bytes(P->K, P->N, T);
 }
 
 extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x, int64_t x_stride,
@@ -377,7 +378,9 @@ extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x,
   if (!linear_supported(P)) return MOE_ERR_UNSUPPORTED;
   if (T < 0) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (T > MOE_MAX_LINEAR_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (T > MOE_MAX_LINEAR_ROWS || x_stride > kLinMaxStride || out_stride > kLinMaxStride ||
+      (mul && mul_stride > kLinMaxStride) || (residual && residual_stride > kLinMaxStride))
+    return MOE_ERR_UNSUPPORTED;
   if (!P->w || !aligned(P->w, 256) || !aligned(P->bias, 4)) return MOE_ERR_INVALID_ARG;
   if (!x || !rows_ok(x, x_stride, P->K)) return MOE_ERR_INVALID_ARG;
   if (mul && !rows_ok(mul, mul_stride, P->N)) return MOE_ERR_INVALID_ARG;
@@ -393,7 +396,7 @@ extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x,
   if (residual && !(residual == out && residual_stride == out_stride) &&
       overlaps(residual, rows_bytes(T, residual_stride, P->N), out, ob))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = lin_ws_layout(P->K, P->N, T).total;
+  const size_t need = lin_ws_bytes(P->K, P->N, T);
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 256) || overlaps(ws, need, out, ob)) return MOE_ERR_INVALID_ARG;
   const PackedLayout pl = packed_layout(P->qtype, P->K, P->N);
@@ -401,7 +404,7 @@ extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x,
                      mul,                  residual,  out,       x_stride, mul_stride,
                      residual_stride,      out_stride, P->K,     P->N,     P->qtype,
                      P->act};
-  return launch_linear(A, T, (uint8_t*)ws, stream) ? MOE_ERR_DEVICE : MOE_OK;
+  return launch_linear(A, T, stream) ? MOE_ERR_DEVICE : MOE_OK;
 }
 
 extern "C" const char* moe_status_string(moe_status s) {

@@ -9,8 +9,8 @@
 //     each 32-group's partial sum multiplied by its fp16 scale in fp32, K
 //     split over the waves of a block.  One launch.
 //   many rows: bound by the matrix cores.  The scale goes into an fp16
-//     operand, so that one 32x32x16 op follows another over the whole of K.
-//     Rows and columns are first given powers of two (staging launch).
+//     operand, so that one 32x32x16 op follows another over the whole of K,
+//     and the rows are turned to fp16 on their way into LDS.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -21,7 +21,6 @@
 namespace bqmoe {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void lds_void;
 
 // --------------------------------------------------------------- epilogue
 __device__ __forceinline__ float sigmoid_f(float v) {
@@ -29,52 +28,48 @@ __device__ __forceinline__ float sigmoid_f(float v) {
 }
 
 // act(v) in fp32 (exponential and reciprocal by the hardware, one unit in the
-// last place each; the result is rounded to bf16 right after)
-__device__ __forceinline__ float activate(int act, float v) {
-  switch (act) {
-    case MOE_ACT_SILU: return v * sigmoid_f(v);
-    case MOE_ACT_GELU: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case MOE_ACT_GELU_TANH:
-      return v * sigmoid_f(1.5957691216057308f * (v + 0.044715f * v * v * v));
-    case MOE_ACT_RELU: return v < 0.f ? 0.f : v;
-    case MOE_ACT_RELU2: return v < 0.f ? 0.f : v * v;
-    case MOE_ACT_SIGMOID: return sigmoid_f(v);
+// last place each; the result is rounded to bf16 right after).  The erf of
+// GELU is Abramowitz and Stegun's 7.1.26 (absolute error 1.5e-7), in the form
+// that gives erfc(|z|) = poly(t) exp(-z^2), t = 1 / (1 + 0.3275911 |z|).
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if (ACT == MOE_ACT_SILU) return v * sigmoid_f(v);
+  if (ACT == MOE_ACT_GELU) {
+    const float z = fabsf(v) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, z, 1.0f));
+    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f),
+                                     -0.284496736f), 0.254829592f);
+    const float c = 0.5f * p * __builtin_amdgcn_exp2f(-1.4426950408889634f * z * z);
+    return v * (v < 0.f ? c : 1.0f - c);
   }
+  if (ACT == MOE_ACT_GELU_TANH)
+    return v * sigmoid_f(1.5957691216057308f * (v + 0.044715f * v * v * v));
+  if (ACT == MOE_ACT_RELU) return v < 0.f ? 0.f : v;
+  if (ACT == MOE_ACT_RELU2) return v < 0.f ? 0.f : v * v;
+  if (ACT == MOE_ACT_SIGMOID) return sigmoid_f(v);
   return v;
+}
+
+// f(integral constant of the activation): one copy of f's code for each
+template <typename F>
+__device__ __forceinline__ void for_act(int act, F f) {
+  switch (act) {
+    case MOE_ACT_SILU: f(std::integral_constant<int, MOE_ACT_SILU>{}); break;
+    case MOE_ACT_GELU: f(std::integral_constant<int, MOE_ACT_GELU>{}); break;
+    case MOE_ACT_GELU_TANH: f(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
+    case MOE_ACT_RELU: f(std::integral_constant<int, MOE_ACT_RELU>{}); break;
+    case MOE_ACT_RELU2: f(std::integral_constant<int, MOE_ACT_RELU2>{}); break;
+    case MOE_ACT_SIGMOID: f(std::integral_constant<int, MOE_ACT_SIGMOID>{}); break;
+    default: break;
+  }
 }
 
 __device__ __forceinline__ void finish(const LinArgs& A, float v, int t, int n) {
   if (A.bias) v += A.bias[n];
-  v = activate(A.act, v);
+  for_act(A.act, [&](auto ac) { v = activate<decltype(ac)::value>(v); });
   if (A.mul) v *= bf16_to_f32(A.mul[(int64_t)t * A.ldm + n]);
   if (A.res) v += bf16_to_f32(A.res[(int64_t)t * A.ldr + n]);
   A.out[(int64_t)t * A.ldo + n] = (uint16_t)f32_to_bf16(v);
-}
-
-// Eight consecutive columns at once (16-byte loads and stores).
-__device__ __forceinline__ void finish8(const LinArgs& A, float (&v)[8], int t, int n) {
-  if (A.bias) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += A.bias[n + j];
-  }
-  if (A.act != MOE_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate(A.act, v[j]);
-  }
-  if (A.mul) {
-    const u32x4 m = *reinterpret_cast<const u32x4*>(A.mul + (int64_t)t * A.ldm + n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-  }
-  if (A.res) {
-    const u32x4 m = *reinterpret_cast<const u32x4*>(A.res + (int64_t)t * A.ldr + n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-  }
-  u32x4 o;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
-  *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
 }
 
 // --------------------------------------------------------------- few rows
@@ -204,65 +199,6 @@ __global__ __launch_bounds__(512) void k_lin_few(LinArgs A, LevelK lk, int T) {
 }
 
 // --------------------------------------------------------------- many rows
-// Staging.  One wave per row: e = (exponent of max|x|) - 14, in [-100, 114];
-// xs = fp16(x * 2^-e), exact for values down to 2^-31 of the row's maximum,
-// rscale = 2^e.  The blocks after the rows take 256 columns each: cscale =
-// 2^-f, where 2^f (in fp16, f at most 15) brings the column's largest |scale|
-// to [2^13, 2^14), so that scale * level keeps 11 bits however small a
-// column's scales are.
-__global__ __launch_bounds__(256) void k_lin_stage(LinArgs A, int T, uint16_t* __restrict__ xs,
-                                                   float* __restrict__ rscale,
-                                                   float* __restrict__ cscale, int row_blocks) {
-  const int K = A.K;
-  if ((int)blockIdx.x >= row_blocks) {
-    const int n = ((int)blockIdx.x - row_blocks) * 256 + threadIdx.x;
-    if (n >= A.N) return;
-    const int KB = K / 128;
-    const uint8_t* sc = A.w + A.scales + (size_t)(n >> 4) * KB * 128 + (n & 15) * 8;
-    uint32_t m = 0;
-    for (int kb = 0; kb < KB; ++kb) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(sc + (size_t)kb * 128);
-      m = max(m, max(max(v[0] & 0x7FFFu, (v[0] >> 16) & 0x7FFFu),
-                     max(v[1] & 0x7FFFu, (v[1] >> 16) & 0x7FFFu)));
-    }
-    // exponent of the largest scale (a subnormal one counts as 2^-15, an
-    // infinite or zero one leaves the column as it is)
-    const int ex = (int)(m >> 10) - 15;
-    const int f = m == 0 || m >= 0x7C00u ? 0 : min(15, 13 - ex);
-    cscale[n] = __uint_as_float((uint32_t)(127 - f) << 23);
-    return;
-  }
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (row >= T) return;
-  const uint16_t* s = A.x + (int64_t)row * A.ldx;
-  uint16_t* d = xs + (size_t)row * K;
-  uint32_t m = 0;
-  for (int i = lane * 8; i < K; i += 512) {
-    const uint4 v = *reinterpret_cast<const uint4*>(s + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
-  const int e = min(114, max(-100, (int)(m >> 7) - 127 - 14));
-  const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-  for (int i = lane * 8; i < K; i += 512) {
-    const uint4 v = *reinterpret_cast<const uint4*>(s + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const _Float16 lo = (_Float16)(bf16_to_f32(w[j] & 0xFFFFu) * f);
-      const _Float16 hi = (_Float16)(bf16_to_f32(w[j] >> 16) * f);
-      o[j] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
-             ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
-    }
-    *reinterpret_cast<uint4*>(d + i) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  if (lane == 0) rscale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
-}
-
 // Weight operand of one lane: 8 values of one column and 32-group GB as fp16,
 // s * (u - offset) * fac with fac = 1, 1/2, 1/4 (ternary, 2-bit, 3-bit; so
 // that no factor overflows): a mask-and-or puts the level into the mantissa of
@@ -317,28 +253,150 @@ constexpr int wait_vm_lgkm(int vm, int lgkm) {
 
 constexpr int kRsrcLin = 0x00020000;  // buffer resource word 3: raw 32-bit dwords
 
-// 64 lanes x 16 bytes straight into LDS, lane l's at at + 16 l
-__device__ __forceinline__ void load_lds16(const void* base, uint8_t* at, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, kRsrcLin), (lds_void*)at,
-      16, off, soff, 0, 0);
+// 16, 8 or 4 bytes per lane at base + off + soff
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, -1, kRsrcLin);
+}
+__device__ __forceinline__ u32x4 load_b128(const void* base, int off, int soff) {
+  return __builtin_bit_cast(u32x4,
+                            __builtin_amdgcn_raw_buffer_load_b128(rsrc_of(base), off, soff, 0));
+}
+__device__ __forceinline__ u32x2 load_b64(const void* base, int off, int soff) {
+  return __builtin_bit_cast(u32x2,
+                            __builtin_amdgcn_raw_buffer_load_b64(rsrc_of(base), off, soff, 0));
+}
+__device__ __forceinline__ uint32_t load_b32(const void* base, int off, int soff) {
+  return __builtin_amdgcn_raw_buffer_load_b32(rsrc_of(base), off, soff, 0);
+}
+
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                __builtin_bit_cast(u16x2, b)));
+}
+
+// Epilogue of the matrix-core kernels: register i of acc[rt][ct] is row
+// rt*32 + 8(i/4) + 4(lane/32) + i%4 and column l32 of its 32 x 32 tile.  Bias
+// and activation are applied there; then each wave turns 32 rows of its
+// columns at a time in LDS of its own, so that a lane holds 8 consecutive
+// columns and whole cache lines are read and written.  The factor (or, without
+// one, the residual) of the next 32 rows is loaded meanwhile.  srow: the tile
+// rows' powers of two in LDS; cscale: those of the lane's columns.
+template <int CT>
+constexpr int kTurnRow = 32 * CT + 8;  // floats; rows 4 apart are half the banks apart
+template <int CT>
+constexpr int kTurnBytes = 32 * kTurnRow<CT> * 4;
+
+template <int NRT, int CT>
+__device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][CT], float unfac,
+                                           const float* srow, const float (&cscale)[CT],
+                                           uint8_t* area, int T, int row0, int col0) {
+  constexpr int kLanes = 4 * CT, kRows = 64 / kLanes, P = 32 / kRows;  // lanes a row, passes
+  const int lane = threadIdx.x & 63, l32 = lane & 31, hl = lane >> 5;
+  float* const turn = reinterpret_cast<float*>(area);
+  const int lr = lane / kLanes, n = col0 + 8 * (lane % kLanes);
+  const uint16_t* const first = A.mul ? A.mul : A.res;
+  const int64_t ldf = A.mul ? A.ldm : A.ldr;
+  const bool second = A.mul && A.res;
+  u32x4 op[2][P], op2[P];
+  auto fetch = [&](const uint16_t* base, int64_t ld, int rt, u32x4 (&o)[P])
+      __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int t = row0 + rt * 32 + p * kRows + lr;
+      o[p] = u32x4{0u, 0u, 0u, 0u};
+      if (t < T && n < A.N) o[p] = *reinterpret_cast<const u32x4*>(base + (int64_t)t * ld + n);
+    }
+  };
+  if (first) fetch(first, ldf, 0, op[0]);
+  float cs[CT], bi[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = min(col0 + 32 * ct + l32, A.N - 1);
+    cs[ct] = unfac * cscale[ct];
+    bi[ct] = A.bias ? A.bias[c] : 0.f;
+  }
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 rs = *reinterpret_cast<const f32x4*>(srow + rt * 32 + 8 * j + 4 * hl);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          acc[rt][ct][4 * j + i] = acc[rt][ct][4 * j + i] * cs[ct] * rs[i] + bi[ct];
+    }
+  for_act(A.act, [&](auto ac) __attribute__((always_inline)) {
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[rt][ct][i] = activate<decltype(ac)::value>(acc[rt][ct][i]);
+  });
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    if (second) fetch(A.res, A.ldr, rt, op2);
+    if (rt + 1 < NRT && first) fetch(first, ldf, rt + 1, op[(rt + 1) & 1]);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        turn[(8 * (i >> 2) + 4 * hl + (i & 3)) * kTurnRow<CT> + 32 * ct + l32] = acc[rt][ct][i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int m = p * kRows + lr, t = row0 + rt * 32 + m;
+      const float* at = turn + m * kTurnRow<CT> + 8 * (lane % kLanes);
+      const f32x4 v0 = *reinterpret_cast<const f32x4*>(at);
+      const f32x4 v1 = *reinterpret_cast<const f32x4*>(at + 4);
+      float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = bf16_to_f32((op[rt & 1][p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+        if (A.mul)
+          v[j] *= f;
+        else if (first)
+          v[j] += f;
+        if (second) v[j] += bf16_to_f32((op2[p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+      }
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
+      if (t < T && n < A.N) *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
 }
 
 // Block: a tile of 32 NRT rows and W waves of 32 CT columns each.  Per 128-wide
-// k-step the block's fp16 rows go into a ring of three LDS stages (direct
-// loads two steps ahead), each wave's packed words and scales into registers
-// one step ahead; the wave builds its weight operands in registers, each
-// feeding NRT matrix-core ops.
+// k-step the block's rows go through registers into one of two LDS stages as
+// fp16 (a step ahead), each wave's packed words and scales into registers one
+// step ahead; the wave builds its weight operands in registers, each feeding
+// NRT matrix-core ops.
+//
+// fp16 holds a bf16 value exactly down to 2^-17 and rounds smaller ones by at
+// most 2^-24, and it holds scale * 2^6 * level with 11 bits down to 2^-14.  So
+// where each row's largest value is 0 or lies in [2^-6, 2^15] and each
+// column's largest scale is 0 or in [2^-14, 2^10], plain conversion loses
+// nothing that counts.  The block learns both maxima on the way; if one is
+// outside, it runs the product again with each row's values and each column's
+// scales brought to the upper end of the range by powers of two (pass 2).
+// (Giving every row its power of two beforehand took a launch of its own that
+// read and wrote all rows: 46 us of 180 at 8192 x 4096 x 2048.)
 template <int Q, int NRT, int W, int CT>
-__global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk,
-                                                        const uint16_t* __restrict__ xs,
-                                                        const float* __restrict__ rscale,
-                                                        const float* __restrict__ cscale, int T,
+__global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, int T,
                                                         int row_tiles, int ncol) {
   extern __shared__ __attribute__((aligned(16))) uint8_t sbuf[];
-  constexpr int R = 32 * NRT, kStage = R * 256, kDma = R / (4 * W);
-  static_assert(R % (4 * W) == 0, "row split");
+  constexpr int R = 32 * NRT, kStage = R * 256, kCh = R / (4 * W);
+  static_assert(R % (4 * W) == 0 && kCh <= 8, "row split");
   constexpr bool Q3 = Q == MOE_Q_INT3;
+  __shared__ __attribute__((aligned(16))) float srow[R];
+  __shared__ int s_redo;
   // work item = (row tile, column group), tile-major; each XCD takes one
   // contiguous chunk of the items (blocks go to the 8 XCDs round-robin)
   const int n_items = row_tiles * ncol, chunk = (n_items + 7) / 8;
@@ -347,19 +405,22 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk,
   const int tile = item / ncol, col = item % ncol;
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, hl = lane >> 5, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int K = A.K, N = A.N, S = K / 128, NT = N / 16;
+  const int K = A.K, S = K / 128, NT = A.N / 16;
   const int row0 = tile * R;
+  if (tid == 0) s_redo = 0;
 
   // LDS: row i of a stage at i * 256, its 16-byte chunk c (8 k) in slot
-  // c ^ (i % 16); 16 lanes load one row.  Rows past T repeat the last one.
-  const uint16_t* const xrow = xs + (size_t)row0 * K;
-  uint32_t aoffs[kDma];
+  // c ^ (i % 16); 16 lanes convert one row.  Rows past T repeat the last one.
+  const uint16_t* const xrow = A.x + (int64_t)row0 * A.ldx;
+  uint32_t xo[kCh];
 #pragma unroll
-  for (int i = 0; i < kDma; ++i) {
-    const int row = 4 * kDma * wave + 4 * i + (lane >> 4);
-    aoffs[i] = (uint32_t)min(row, T - 1 - row0) * (uint32_t)(2 * K) +
-               (((lane & 15) ^ (row & 15)) << 4);
+  for (int i = 0; i < kCh; ++i) {
+    const int row = 4 * (kCh * wave + i) + (lane >> 4);
+    xo[i] = (uint32_t)min(row, T - 1 - row0) * (uint32_t)(2 * A.ldx) + (lane & 15) * 16;
   }
+  // (rows 4 i on: the swizzle's 4 i is XORed in where a chunk is stored)
+  const uint32_t lo = (uint32_t)((4 * kCh * wave + (lane >> 4)) * 256) |
+                      (((lane & 15) ^ (((4 * kCh * wave) & 15) + (lane >> 4))) << 4);
   const uint32_t la = (uint32_t)(l32 * 256) | ((uint32_t)(hl ^ (l32 & 15)) << 4);
 
   OperandK k = kk;
@@ -370,7 +431,6 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk,
   // packed weights: column tile ct of the wave is n-tiles 2c, 2c + 1 of
   // c = (col W + wave) CT + ct; tiles past N repeat the last one (not stored)
   uint32_t wo[CT], po[CT], so[CT];
-  uint32_t cm[CT];  // 2^f of the lane's column, twice
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
     const int c32 = (col * W + wave) * CT + ct;
@@ -378,42 +438,28 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk,
     wo[ct] = nt * S * 512 + (16 * hl + r) * 8;
     po[ct] = (uint32_t)A.plane1 + nt * S * 256 + (16 * hl + r) * 4;
     so[ct] = (uint32_t)A.scales + nt * S * 128 + r * 8;
-    const uint32_t ex = (__float_as_uint(cscale[nt * 16 + r]) >> 23) & 0xFFu;  // 127 - f
-    const uint32_t h = (127u + 15u - ex) << 10;
-    cm[ct] = h | (h << 16);
   }
-
-  f32x16 acc[NRT][CT];
-#pragma unroll
-  for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
 
   struct Words {
     u32x2 w[CT][2], s[CT];
     uint32_t w1[CT][2];
   };
-  auto issue = [&](int s, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kDma; ++i)
-      load_lds16(xrow, sbuf + buf * kStage + (kDma * wave + i) * 1024, aoffs[i], s * 256);
+  u32x4 xv[kCh];               // bf16 rows of the step after the next
+  float rmax[kCh], rfac[kCh];  // the rows' largest |x| so far, 2^-e of pass 2
+  uint32_t cmax[CT], cm[CT];   // the column's largest |scale| (two halves), 2^f twice
+  f32x16 acc[NRT][CT];
+  auto loadx = [&](int s, int i) __attribute__((always_inline)) {
+    xv[i] = load_b128(xrow, (int)xo[i], min(s, S - 1) * 256);
   };
   auto loadb = [&](int s, Words& b) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t rB =
-        __builtin_amdgcn_make_buffer_rsrc((void*)A.w, 0, -1, kRsrcLin);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        b.w[ct][h] = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_raw_buffer_load_b64(rB, (int)wo[ct], s * 512 + 256 * h, 0));
-        if (Q3)
-          b.w1[ct][h] = __builtin_amdgcn_raw_buffer_load_b32(rB, (int)po[ct], s * 256 + 128 * h, 0);
+        b.w[ct][h] = load_b64(A.w, (int)wo[ct], s * 512 + 256 * h);
+        if (Q3) b.w1[ct][h] = load_b32(A.w, (int)po[ct], s * 256 + 128 * h);
       }
-      b.s[ct] = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_raw_buffer_load_b64(rB, (int)so[ct], s * 128, 0));
+      b.s[ct] = load_b64(A.w, (int)so[ct], s * 128);
     }
   };
   auto build = [&](auto qc, const Words& b, u32x4 (&o)[CT]) __attribute__((always_inline)) {
@@ -431,130 +477,162 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk,
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) a[rt] = *reinterpret_cast<const u32x4*>(p + rt * 8192);
   };
-  auto mfmas = [&](const u32x4 (&a)[NRT], const u32x4 (&b)[CT]) __attribute__((always_inline)) {
+
+  // One product over K; SCALED: pass 2.
+  auto product = [&](auto scaled) __attribute__((always_inline)) {
+    constexpr bool SC = decltype(scaled)::value;
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mfma_lin(a[rt], b[ct], acc[rt][ct]);
-  };
-  // sub-step q of a step (group q/2, k-half q%2): the next sub-step's rows are
-  // read and its weights built while this one's matrix-core ops run
-  auto sub = [&](auto qc, uint32_t at, const Words& b, const Words& bn, u32x4 (&a0)[NRT],
-                 u32x4 (&a1)[NRT], u32x4 (&o0)[CT], u32x4 (&o1)[CT])
-      __attribute__((always_inline)) {
-    constexpr int q = decltype(qc)::value;
-    if constexpr (q < 7) loada(at, q + 1, a1);
-    if constexpr (q < 7)
-      build(std::integral_constant<int, q + 1>{}, b, o1);
-    else
-      build(std::integral_constant<int, 0>{}, bn, o1);
-    mfmas(a0, o0);
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int i = 0; i < NRT * CT; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, Q3 ? 7 : 5, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
+    // chunk i of xv as fp16 into LDS stage st
+    auto convert = [&](int i, int st) __attribute__((always_inline)) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a = __uint_as_float(xv[i][j] << 16), b = __uint_as_float(xv[i][j] & 0xFFFF0000u);
+        if (SC) {
+          a *= rfac[i];
+          b *= rfac[i];
+        } else {
+          rmax[i] = fmaxf(rmax[i], fmaxf(fabsf(a), fabsf(b)));
+        }
+        o[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+      }
+      *reinterpret_cast<u32x4*>(sbuf + st * kStage + i * 1024 + (lo ^ ((i & 3) << 6))) = o;
+    };
+    // sub-step q of a step (group q/2, k-half q%2): the next sub-step's rows
+    // are read, its weights built and a part of the next step's rows
+    // converted while this one's matrix-core ops run
+    auto sub = [&](auto qc, int s, uint32_t at, const Words& b, const Words& bn, u32x4 (&a0)[NRT],
+                   u32x4 (&a1)[NRT], u32x4 (&o0)[CT], u32x4 (&o1)[CT])
+        __attribute__((always_inline)) {
+      constexpr int q = decltype(qc)::value;
+      if constexpr (q < 7) loada(at, q + 1, a1);
+      if constexpr (q < 7)
+        build(std::integral_constant<int, q + 1>{}, b, o1);
+      else
+        build(std::integral_constant<int, 0>{}, bn, o1);
+      if constexpr (q < kCh) convert(q, (s + 1) & 1);
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) acc[rt][ct] = mfma_lin(a0[rt], o0[ct], acc[rt][ct]);
+#pragma unroll
+      for (int i = 0; i < NRT * CT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, Q3 ? 8 : 6, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (q < kCh) loadx(s + 2, q);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    Words wa, wb;
+    u32x4 a0[NRT], a1[NRT], o0[CT], o1[CT];
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) loadx(0, i);
+    loadb(0, wa);
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) convert(i, 0);
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) loadx(1, i);
+    build(std::integral_constant<int, 0>{}, wa, o0);
+    auto step = [&](int s, const Words& b, Words& bn) __attribute__((always_inline)) {
+      // step s's rows are in LDS for every wave, and every wave is done with
+      // the stage that step s + 1's overwrite
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm(63, 0));
+      __builtin_amdgcn_s_barrier();
+      const uint32_t at = la + (uint32_t)((s & 1) * kStage);
+      loada(at, 0, a0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (!SC) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) cmax[ct] = pk_max_u16(cmax[ct], b.s[ct][i] & 0x7FFF7FFFu);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      sub(std::integral_constant<int, 0>{}, s, at, b, bn, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 1>{}, s, at, b, bn, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 2>{}, s, at, b, bn, a0, a1, o0, o1);
+      // the next step's words, where half of this one's are done with (past
+      // the last step they repeat it, so that there is no branch)
+      loadb(min(s + 1, S - 1), bn);
+      __builtin_amdgcn_sched_barrier(0);
+      sub(std::integral_constant<int, 3>{}, s, at, b, bn, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 4>{}, s, at, b, bn, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 5>{}, s, at, b, bn, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 6>{}, s, at, b, bn, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 7>{}, s, at, b, bn, a1, a0, o1, o0);
+    };
+    int s = 0;
+    for (; s + 1 < S; s += 2) {
+      step(s, wa, wb);
+      step(s + 1, wb, wa);
     }
-    __builtin_amdgcn_sched_barrier(0);
+    if (s < S) step(s, wa, wb);
+    __syncthreads();  // the stages are free
   };
-  Words wa, wb;
-  u32x4 a0[NRT], a1[NRT], o0[CT], o1[CT];
-  issue(0, 0);
-  loadb(0, wa);
-  issue(min(1, S - 1), 1);
-  build(std::integral_constant<int, 0>{}, wa, o0);
-  int st = 0;  // ring stage of step s
-  auto step = [&](int s, const Words& b, Words& bn) __attribute__((always_inline)) {
-    // step s is in LDS for every wave (step s + 1's direct loads may remain in
-    // flight) and every wave is done with step s - 1's stage, which the loads
-    // of step s + 2 overwrite
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm(kDma, 0));
-    __builtin_amdgcn_s_barrier();
-    const int st2 = st == 0 ? 2 : st - 1;
-    const uint32_t at = la + (uint32_t)(st * kStage);
-    loada(at, 0, a0);
-    __builtin_amdgcn_sched_barrier(0);
-    // loads past the last step repeat it, so that a step has no branch
-    loadb(min(s + 1, S - 1), bn);
-    issue(min(s + 2, S - 1), st2);
-    __builtin_amdgcn_sched_barrier(0);
-    sub(std::integral_constant<int, 0>{}, at, b, bn, a0, a1, o0, o1);
-    sub(std::integral_constant<int, 1>{}, at, b, bn, a1, a0, o1, o0);
-    sub(std::integral_constant<int, 2>{}, at, b, bn, a0, a1, o0, o1);
-    sub(std::integral_constant<int, 3>{}, at, b, bn, a1, a0, o1, o0);
-    sub(std::integral_constant<int, 4>{}, at, b, bn, a0, a1, o0, o1);
-    sub(std::integral_constant<int, 5>{}, at, b, bn, a1, a0, o1, o0);
-    sub(std::integral_constant<int, 6>{}, at, b, bn, a0, a1, o0, o1);
-    sub(std::integral_constant<int, 7>{}, at, b, bn, a1, a0, o1, o0);
-    st = st == 2 ? 0 : st + 1;
-  };
-  int s = 0;
-  for (; s + 1 < S; s += 2) {
-    step(s, wa, wb);
-    step(s + 1, wb, wa);
-  }
-  if (s < S) step(s, wa, wb);
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm(0, 0));  // the repeated last loads have landed
 
-  // Epilogue: register i of acc[rt][ct] is row rt*32 + 8(i/4) + 4 hl + i%4,
-  // column l32.  Each wave turns 64 x 32 results at a time in LDS of its own
-  // (rows 40 floats apart, free of bank conflicts), so that a lane finishes 8
-  // consecutive columns.
-  __builtin_amdgcn_s_barrier();  // the ring is free
-  constexpr int kTurn = 40, kRt = NRT < 2 ? 1 : 2;
-  static_assert(W * kRt * 32 * kTurn * 4 <= 3 * kStage && NRT % kRt == 0, "turning area");
-  float* const turn = reinterpret_cast<float*>(sbuf) + wave * kRt * 32 * kTurn;
-  constexpr float unfac = Q == MOE_Q_TERNARY ? 1.f : Q == MOE_Q_INT2 ? 2.f : 4.f;
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) rmax[i] = 0.f;
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) {
-    const int n0 = ((col * W + wave) * CT + ct) * 32;
-    const float cs = unfac * cscale[min(n0 + l32, N - 1)];
-#pragma unroll
-    for (int r0 = 0; r0 < NRT; r0 += kRt) {
-#pragma unroll
-      for (int rt = 0; rt < kRt; ++rt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          turn[(rt * 32 + 8 * (i >> 2) + 4 * hl + (i & 3)) * kTurn + l32] = acc[r0 + rt][ct][i] * cs;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      const int n = n0 + 8 * (lane & 3);
-#pragma unroll 1
-      for (int p = 0; p < 2 * kRt; ++p) {
-        const int m = 16 * p + (lane >> 2), t = row0 + r0 * 32 + m;
-        if (t < T && n < N) {
-          const f32x4 v0 = *reinterpret_cast<const f32x4*>(turn + m * kTurn + 8 * (lane & 3));
-          const f32x4 v1 = *reinterpret_cast<const f32x4*>(turn + m * kTurn + 8 * (lane & 3) + 4);
-          const float rs = rscale[t];
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[j] = v0[j] * rs;
-            v[4 + j] = v1[j] * rs;
-          }
-          finish8(A, v, t, n);
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
+    cmax[ct] = 0u;
+    cm[ct] = 0x54005400u;  // 2^6
   }
+  product(std::false_type{});
+
+  // the maxima: rows over their 16 lanes, columns over the two halves
+  constexpr float unfac = Q == MOE_Q_TERNARY ? 1.f : Q == MOE_Q_INT2 ? 2.f : 4.f;
+  float cscale[CT];
+  bool redo = false;
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) rmax[i] = fmaxf(rmax[i], __shfl_xor(rmax[i], o, 64));
+    redo |= rmax[i] != 0.f && !(rmax[i] >= 0x1p-6f && rmax[i] <= 0x1p15f);
+    if ((lane & 15) == 0) srow[4 * (kCh * wave + i) + (lane >> 4)] = 1.f;
+  }
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    cmax[ct] = max(cmax[ct] & 0xFFFFu, cmax[ct] >> 16);
+    redo |= cmax[ct] != 0u && !(cmax[ct] >= 0x0400u && cmax[ct] <= 0x6400u);
+    cscale[ct] = 0x1p-6f;
+  }
+  if (redo) s_redo = 1;
+  __syncthreads();
+  if (s_redo) {
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) {
+      // 2^e brings the largest value to [2^14, 2^15); an infinite one counts as 2^114
+      const int e = min(114, max(-100, (int)(__float_as_uint(rmax[i]) >> 23) - 127 - 14));
+      rfac[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+      if ((lane & 15) == 0)
+        srow[4 * (kCh * wave + i) + (lane >> 4)] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      // 2^f brings the largest scale to [2^13, 2^14) (f at most 15: a subnormal
+      // one to 2^-9 at least); an infinite or zero one leaves the column as it is
+      const int f = cmax[ct] == 0u || cmax[ct] >= 0x7C00u
+                        ? 0
+                        : min(15, 13 - ((int)(cmax[ct] >> 10) - 15));
+      cm[ct] = (uint32_t)(f + 15) << 10;
+      cm[ct] |= cm[ct] << 16;
+      cscale[ct] = __uint_as_float((uint32_t)(127 - f) << 23);
+    }
+    product(std::true_type{});
+  }
+  store_tile<NRT, CT>(A, acc, unfac, srow, cscale, sbuf + wave * kTurnBytes<CT>, T, row0,
+                      (col * W + wave) * CT * 32);
 }
 
 // ------------------------------------------------------------------ launch
-LinWs lin_ws_layout(int K, int N, int T) {
-  LinWs w{};
-  if (T <= kLinFewRows) {
-    w.total = 256;
-    return w;
-  }
-  const auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
-  w.xs = 0;
-  w.rscale = up((size_t)T * K * 2);
-  w.cscale = up(w.rscale + (size_t)T * 4);
-  w.total = up(w.cscale + (size_t)N * 4);
-  return w;
-}
+size_t lin_ws_bytes(int, int, int) { return 256; }
 
 template <bool Q3>
 static void few(const LinArgs& A, int T, hipStream_t s) {
@@ -586,28 +664,22 @@ static void few(const LinArgs& A, int T, hipStream_t s) {
 }
 
 template <int Q, int NRT, int W, int CT>
-static int gemm(const LinArgs& A, const OperandK& k, int T, uint8_t* ws, const LinWs& L,
-                hipStream_t s) {
+static int gemm(const LinArgs& A, const OperandK& k, int T, hipStream_t s) {
   const int tiles = (T + 32 * NRT - 1) / (32 * NRT), ncol = (A.N + 32 * CT * W - 1) / (32 * CT * W);
-  const size_t lds = 3 * 32 * NRT * 256;
-  if (lds > 65536 &&
+  constexpr size_t stages = 2 * 32 * NRT * 256, turn = W * kTurnBytes<CT>;
+  constexpr size_t lds = stages > turn ? stages : turn;
+  if (lds > 64000 &&
       hipFuncSetAttribute((const void*)k_lin_gemm<Q, NRT, W, CT>,
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
     return (int)hipErrorInvalidConfiguration;
   const int items = tiles * ncol;
   hipLaunchKernelGGL((k_lin_gemm<Q, NRT, W, CT>), dim3((items + 7) / 8 * 8), dim3(64 * W), lds, s,
-                     A, k, (const uint16_t*)(ws + L.xs), (const float*)(ws + L.rscale),
-                     (const float*)(ws + L.cscale), T, tiles, ncol);
+                     A, k, T, tiles, ncol);
   return (int)hipGetLastError();
 }
 
 template <int Q>
-static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
-  const LinWs L = lin_ws_layout(A.K, A.N, T);
-  const int row_blocks = (T + 3) / 4;
-  hipLaunchKernelGGL(k_lin_stage, dim3(row_blocks + (A.N + 255) / 256), dim3(256), 0, s, A, T,
-                     (uint16_t*)(ws + L.xs), (float*)(ws + L.rscale), (float*)(ws + L.cscale),
-                     row_blocks);
+static int many(const LinArgs& A, int T, hipStream_t s) {
   // -(base + offset) * fac for the bases 256, 64, 16
   OperandK k = {0x000C000Cu, 0x00300030u, 0x00C000C0u, 0x5C005C00u, 0x54005400u, 0x4C004C00u,
                 0, 0, 0};
@@ -622,11 +694,11 @@ static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
   k.o4 = pair(-(64.f + off) * fac);
   k.o6 = pair(-(16.f + off) * fac);
   const long blocks = (long)((T + 127) / 128) * ((A.N + 511) / 512);
-  if (blocks >= 192) return gemm<Q, 4, 8, 2>(A, k, T, ws, L, s);
-  return gemm<Q, 2, 4, 1>(A, k, T, ws, L, s);
+  if (blocks >= 192) return gemm<Q, 4, 8, 2>(A, k, T, s);
+  return gemm<Q, 2, 4, 1>(A, k, T, s);
 }
 
-int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream) {
+int launch_linear(const LinArgs& A, int T, void* stream) {
   hipStream_t s = (hipStream_t)stream;
   if (T <= kLinFewRows) {
     if (A.q == MOE_Q_INT3)
@@ -635,9 +707,9 @@ int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream) {
       few<false>(A, T, s);
     return (int)hipGetLastError();
   }
-  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, T, ws, s);
-  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, T, ws, s);
-  return many<MOE_Q_INT3>(A, T, ws, s);
+  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, T, s);
+  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, T, s);
+  return many<MOE_Q_INT3>(A, T, s);
 }
 
 }  // namespace bqmoe

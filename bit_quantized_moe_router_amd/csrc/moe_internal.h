@@ -128,15 +128,9 @@ struct LinArgs {
   int64_t ldx, ldm, ldr, ldo;  // row strides in values
   int32_t K, N, q, act;
 };
-struct LinWs {
-  size_t xs;      // fp16 [T][K]  x * 2^-e
-  size_t rscale;  // fp32 [T]     2^e
-  size_t cscale;  // fp32 [N]     2^-f
-  size_t total;
-};
 constexpr int kLinFewRows = 64;  // rows up to which the bandwidth kernel runs
-LinWs lin_ws_layout(int K, int N, int T);
-int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream);
+size_t lin_ws_bytes(int K, int N, int T);
+int launch_linear(const LinArgs& A, int T, void* stream);
 // Whether the decode kernels take this layer for T tokens (LDS and register
 // limits of their launch shapes).
 bool decode_shape_ok(const moe_layer* L, int T);

@@ -349,7 +349,7 @@ typedef enum {
   MOE_ACT_RELU2 = 5,     /* relu(v)^2 */
   MOE_ACT_SIGMOID = 6
 } moe_act;
-enum { MOE_MAX_LINEAR_ROWS = 1 << 24 };
+enum { MOE_MAX_LINEAR_ROWS = 1 << 24, MOE_MAX_LINEAR_STRIDE = 1 << 23 };
 typedef struct {
   int32_t K, N;      /* K % 128 == 0, N % 16 == 0, both up to MOE_MAX_DIM */
   int32_t qtype;     /* moe_qtype of w */
@@ -369,7 +369,8 @@ size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T);
  *              else.  Only the N values of its T rows are written.
  *   ws       : device workspace of ws_bytes >= moe_linear_workspace_bytes(P, T)
  * Rows start at 16-byte aligned addresses: pointers are 16-byte aligned and
- * strides multiples of 8, at least the row's length.
+ * strides multiples of 8, at least the row's length, at most
+ * MOE_MAX_LINEAR_STRIDE.
  * Errors: MOE_ERR_UNSUPPORTED for a shape or family outside the packed format
  * or the limits above, MOE_ERR_WORKSPACE for a missing or short workspace,
  * MOE_ERR_INVALID_ARG otherwise. */
