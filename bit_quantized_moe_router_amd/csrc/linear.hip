@@ -200,21 +200,24 @@ __global__ __launch_bounds__(512) void k_lin_few(LinArgs A, LevelK lk, int T) {
 
 // --------------------------------------------------------------- many rows
 // Weight operand of one lane: 8 values of one column and 32-group GB as fp16,
-// s * (u - offset) * fac with fac = 1, 1/2, 1/4 (ternary, 2-bit, 3-bit; so
-// that no factor overflows): a mask-and-or puts the level into the mantissa of
-// an fp16 base where its lowest bit is worth 1 (bit 2 under 256, bit 4 under
-// 64, bit 6 under 16), one packed FMA gives (u - offset) * fac exactly, one
-// packed multiply by the scale rounds to fp16's 11 bits.  That rounding is
-// exact for ternary weights and at most 2^-12 of a 2- or 3-bit weight
-// otherwise: an error of about 1e-4 of the result's size, against 1.7e-3 of
-// its rounding to bf16; keeping the scales out of the operand would cost a
-// vector FMA per result and 32-group, as much time as the matrix cores'.
+// s * (u - offset) * fac, fac = 32 (16 for 3-bit levels: then the largest
+// weight of a scale up to 2^10 is finite).  A mask-and-or puts the level into
+// the mantissa of an fp16 base where its lowest bit is worth 1 (bit 2 under
+// 256, bit 4 under 64, bit 6 under 16), one packed FMA gives (u - offset) * fac
+// exactly, one packed multiply by the scale (half GB%2 of sp, for both halves
+// by operand selection) rounds to fp16's 11 bits.  That rounding is exact for
+// ternary weights and at most 2^-12 of a 2- or 3-bit weight otherwise: an
+// error of about 1e-4 of the result's size, against 1.7e-3 of its rounding to
+// bf16; keeping the scales out of the operand would cost a vector FMA per
+// result and 32-group, as much time as the matrix cores'.
 struct OperandK {
   uint32_t m2, m4, m6, b2, b4, b6, o2, o4, o6;
 };
+template <int Q>
+constexpr float kFac = Q == MOE_Q_INT3 ? 16.f : 32.f;
 
 template <int Q, int GB>
-__device__ __forceinline__ u32x4 weights_f16(uint32_t w, uint32_t w1, uint32_t s2,
+__device__ __forceinline__ u32x4 weights_f16(uint32_t w, uint32_t w1, f16x2 sp,
                                              const OperandK& k) {
   const uint32_t x1 = (GB & 1) ? w >> 8 : w, x0 = (GB & 1) ? w >> 6 : w << 2;
   uint32_t f[4] = {(x0 & k.m2) | k.b2, (x1 & k.m2) | k.b2, (x1 & k.m4) | k.b4,
@@ -228,15 +231,13 @@ __device__ __forceinline__ u32x4 weights_f16(uint32_t w, uint32_t w1, uint32_t s
     f[2] = bit_insert(0x00400040u, h12, f[2]);
     f[3] = bit_insert(0x01000100u, h3, f[3]);
   }
-  constexpr uint32_t fac = Q == MOE_Q_INT3 ? 0x34003400u : 0x38003800u;  // 1/4, 1/2
+  const f16x2 s2 = __builtin_shufflevector(sp, sp, GB & 1, GB & 1);
+  const f16x2 fac = {(_Float16)kFac<Q>, (_Float16)kFac<Q>};
   u32x4 r;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const f16x2 o = __builtin_bit_cast(f16x2, v < 2 ? k.o2 : v == 2 ? k.o4 : k.o6);
-    const f16x2 c = Q == MOE_Q_TERNARY
-                        ? __builtin_bit_cast(f16x2, f[v]) + o
-                        : __builtin_bit_cast(f16x2, f[v]) * __builtin_bit_cast(f16x2, fac) + o;
-    r[v] = __builtin_bit_cast(uint32_t, c * __builtin_bit_cast(f16x2, s2));
+    r[v] = __builtin_bit_cast(uint32_t, (__builtin_bit_cast(f16x2, f[v]) * fac + o) * s2);
   }
   return r;
 }
@@ -295,17 +296,17 @@ __device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][
   const int lane = threadIdx.x & 63, l32 = lane & 31, hl = lane >> 5;
   float* const turn = reinterpret_cast<float*>(area);
   const int lr = lane / kLanes, n = col0 + 8 * (lane % kLanes);
+  // rows and columns past the end repeat the last ones (read, not stored)
+  const int nc = min(n, A.N - 8);
   const uint16_t* const first = A.mul ? A.mul : A.res;
   const int64_t ldf = A.mul ? A.ldm : A.ldr;
-  const bool second = A.mul && A.res;
   u32x4 op[2][P], op2[P];
   auto fetch = [&](const uint16_t* base, int64_t ld, int rt, u32x4 (&o)[P])
       __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int t = row0 + rt * 32 + p * kRows + lr;
-      o[p] = u32x4{0u, 0u, 0u, 0u};
-      if (t < T && n < A.N) o[p] = *reinterpret_cast<const u32x4*>(base + (int64_t)t * ld + n);
+      const int t = min(row0 + rt * 32 + p * kRows + lr, T - 1);
+      o[p] = *reinterpret_cast<const u32x4*>(base + (int64_t)t * ld + nc);
     }
   };
   if (first) fetch(first, ldf, 0, op[0]);
@@ -336,41 +337,52 @@ __device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][
         for (int i = 0; i < 16; ++i)
           acc[rt][ct][i] = activate<decltype(ac)::value>(acc[rt][ct][i]);
   });
+  // one straight copy for each of: neither, factor, residual, both
+  auto rows = [&](auto has_mul, auto has_res) __attribute__((always_inline)) {
+    constexpr bool M = decltype(has_mul)::value, S = decltype(has_res)::value;
 #pragma unroll
-  for (int rt = 0; rt < NRT; ++rt) {
-    if (second) fetch(A.res, A.ldr, rt, op2);
-    if (rt + 1 < NRT && first) fetch(first, ldf, rt + 1, op[(rt + 1) & 1]);
+    for (int rt = 0; rt < NRT; ++rt) {
+      if (M && S) fetch(A.res, A.ldr, rt, op2);
+      if ((M || S) && rt + 1 < NRT) fetch(first, ldf, rt + 1, op[(rt + 1) & 1]);
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+      for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        turn[(8 * (i >> 2) + 4 * hl + (i & 3)) * kTurnRow<CT> + 32 * ct + l32] = acc[rt][ct][i];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+        for (int i = 0; i < 16; ++i)
+          turn[(8 * (i >> 2) + 4 * hl + (i & 3)) * kTurnRow<CT> + 32 * ct + l32] = acc[rt][ct][i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int m = p * kRows + lr, t = row0 + rt * 32 + m;
-      const float* at = turn + m * kTurnRow<CT> + 8 * (lane % kLanes);
-      const f32x4 v0 = *reinterpret_cast<const f32x4*>(at);
-      const f32x4 v1 = *reinterpret_cast<const f32x4*>(at + 4);
-      float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+      for (int p = 0; p < P; ++p) {
+        const int m = p * kRows + lr, t = row0 + rt * 32 + m;
+        const float* at = turn + m * kTurnRow<CT> + 8 * (lane % kLanes);
+        const f32x4 v0 = *reinterpret_cast<const f32x4*>(at);
+        const f32x4 v1 = *reinterpret_cast<const f32x4*>(at + 4);
+        float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = bf16_to_f32((op[rt & 1][p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
-        if (A.mul)
-          v[j] *= f;
-        else if (first)
-          v[j] += f;
-        if (second) v[j] += bf16_to_f32((op2[p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+        for (int j = 0; j < 8; ++j) {
+          const float f = bf16_to_f32((op[rt & 1][p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+          if (M) v[j] *= f;
+          if (!M && S) v[j] += f;
+          if (M && S) v[j] += bf16_to_f32((op2[p][j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+        }
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
+        if (t < T && n < A.N) *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
       }
-      u32x4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
-      if (t < T && n < A.N) *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  }
+  };
+  if (!first)
+    rows(std::false_type{}, std::false_type{});
+  else if (!A.res)
+    rows(std::true_type{}, std::false_type{});
+  else if (!A.mul)
+    rows(std::false_type{}, std::true_type{});
+  else
+    rows(std::true_type{}, std::true_type{});
 }
 
 // Block: a tile of 32 NRT rows and W waves of 32 CT columns each.  Per 128-wide
@@ -380,7 +392,7 @@ __device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][
 // NRT matrix-core ops.
 //
 // fp16 holds a bf16 value exactly down to 2^-17 and rounds smaller ones by at
-// most 2^-24, and it holds scale * 2^6 * level with 11 bits down to 2^-14.  So
+// most 2^-24, and the operand keeps 11 bits of a weight of scale down to 2^-17.  So
 // where each row's largest value is 0 or lies in [2^-6, 2^15] and each
 // column's largest scale is 0 or in [2^-14, 2^10], plain conversion loses
 // nothing that counts.  The block learns both maxima on the way; if one is
@@ -462,16 +474,6 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
       b.s[ct] = load_b64(A.w, (int)so[ct], s * 128);
     }
   };
-  auto build = [&](auto qc, const Words& b, u32x4 (&o)[CT]) __attribute__((always_inline)) {
-    constexpr int GB = decltype(qc)::value >> 1, h = decltype(qc)::value & 1;
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-      const uint32_t sh = (b.s[ct][GB >> 1] >> (16 * (GB & 1))) & 0xFFFFu;
-      const uint32_t s2 = __builtin_bit_cast(
-          uint32_t, __builtin_bit_cast(f16x2, sh | (sh << 16)) * __builtin_bit_cast(f16x2, cm[ct]));
-      o[ct] = weights_f16<Q, GB>(b.w[ct][h][GB >> 1], Q3 ? b.w1[ct][h] : 0u, s2, k);
-    }
-  };
   auto loada = [&](uint32_t at, int q, u32x4 (&a)[NRT]) __attribute__((always_inline)) {
     const uint8_t* p = sbuf + (at ^ (uint32_t)((2 * q) << 4));
 #pragma unroll
@@ -487,6 +489,16 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
       for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[rt][ct][i] = 0.f;
+    auto build = [&](auto qc, const Words& b, u32x4 (&o)[CT]) __attribute__((always_inline)) {
+      constexpr int GB = decltype(qc)::value >> 1, h = decltype(qc)::value & 1;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        const uint32_t sw = b.s[ct][GB >> 1];  // (a bit cast of the element itself takes element 0)
+        f16x2 sp = __builtin_bit_cast(f16x2, sw);
+        if (SC) sp = sp * __builtin_bit_cast(f16x2, cm[ct]);
+        o[ct] = weights_f16<Q, GB>(b.w[ct][h][GB >> 1], Q3 ? b.w1[ct][h] : 0u, sp, k);
+      }
+    };
     // chunk i of xv as fp16 into LDS stage st
     auto convert = [&](int i, int st) __attribute__((always_inline)) {
       u32x4 o;
@@ -497,7 +509,8 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
           a *= rfac[i];
           b *= rfac[i];
         } else {
-          rmax[i] = fmaxf(rmax[i], fmaxf(fabsf(a), fabsf(b)));
+          // (the library function would first canonicalise each operand)
+          __asm__("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(rmax[i]) : "v"(a), "v"(b));
         }
         o[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
       }
@@ -580,14 +593,10 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
 #pragma unroll
   for (int i = 0; i < kCh; ++i) rmax[i] = 0.f;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    cmax[ct] = 0u;
-    cm[ct] = 0x54005400u;  // 2^6
-  }
+  for (int ct = 0; ct < CT; ++ct) cmax[ct] = 0u;
   product(std::false_type{});
 
   // the maxima: rows over their 16 lanes, columns over the two halves
-  constexpr float unfac = Q == MOE_Q_TERNARY ? 1.f : Q == MOE_Q_INT2 ? 2.f : 4.f;
   float cscale[CT];
   bool redo = false;
 #pragma unroll
@@ -601,7 +610,7 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
   for (int ct = 0; ct < CT; ++ct) {
     cmax[ct] = max(cmax[ct] & 0xFFFFu, cmax[ct] >> 16);
     redo |= cmax[ct] != 0u && !(cmax[ct] >= 0x0400u && cmax[ct] <= 0x6400u);
-    cscale[ct] = 0x1p-6f;
+    cscale[ct] = 1.f;
   }
   if (redo) s_redo = 1;
   __syncthreads();
@@ -616,18 +625,18 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
     }
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      // 2^f brings the largest scale to [2^13, 2^14) (f at most 15: a subnormal
+      // 2^f brings the largest scale to [2^7, 2^8) (f at most 15: a subnormal
       // one to 2^-9 at least); an infinite or zero one leaves the column as it is
       const int f = cmax[ct] == 0u || cmax[ct] >= 0x7C00u
                         ? 0
-                        : min(15, 13 - ((int)(cmax[ct] >> 10) - 15));
+                        : min(15, 7 - ((int)(cmax[ct] >> 10) - 15));
       cm[ct] = (uint32_t)(f + 15) << 10;
       cm[ct] |= cm[ct] << 16;
       cscale[ct] = __uint_as_float((uint32_t)(127 - f) << 23);
     }
     product(std::true_type{});
   }
-  store_tile<NRT, CT>(A, acc, unfac, srow, cscale, sbuf + wave * kTurnBytes<CT>, T, row0,
+  store_tile<NRT, CT>(A, acc, 1.f / kFac<Q>, srow, cscale, sbuf + wave * kTurnBytes<CT>, T, row0,
                       (col * W + wave) * CT * 32);
 }
 
@@ -689,7 +698,7 @@ static int many(const LinArgs& A, int T, hipStream_t s) {
     __builtin_memcpy(&u, &h, 2);
     return (uint32_t)u | ((uint32_t)u << 16);
   };
-  const float off = qtype_offset(Q), fac = Q == MOE_Q_TERNARY ? 1.f : Q == MOE_Q_INT2 ? .5f : .25f;
+  const float off = qtype_offset(Q), fac = kFac<Q>;
   k.o2 = pair(-(256.f + off) * fac);
   k.o4 = pair(-(64.f + off) * fac);
   k.o6 = pair(-(16.f + off) * fac);
