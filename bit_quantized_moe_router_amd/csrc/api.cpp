@@ -399,12 +399,16 @@ extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x,
   const size_t need = lin_ws_bytes(P->K, P->N, T);
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (!aligned(ws, 256) || overlaps(ws, need, out, ob)) return MOE_ERR_INVALID_ARG;
+  if (overlaps(ws, need, x, rows_bytes(T, x_stride, P->K)) ||
+      (mul && overlaps(ws, need, mul, rows_bytes(T, mul_stride, P->N))) ||
+      (residual && overlaps(ws, need, residual, rows_bytes(T, residual_stride, P->N))))
+    return MOE_ERR_INVALID_ARG;
   const PackedLayout pl = packed_layout(P->qtype, P->K, P->N);
   const LinArgs A = {(const uint8_t*)P->w, pl.plane1, pl.scales, P->bias,  x,
                      mul,                  residual,  out,       x_stride, mul_stride,
                      residual_stride,      out_stride, P->K,     P->N,     P->qtype,
                      P->act};
-  return launch_linear(A, T, stream) ? MOE_ERR_DEVICE : MOE_OK;
+  return launch_linear(A, T, (uint8_t*)ws, stream) ? MOE_ERR_DEVICE : MOE_OK;
 }
 
 extern "C" const char* moe_status_string(moe_status s) {

@@ -4,10 +4,13 @@
 // include/moe.h.  (The pages name the code families of the weights, "Xolotl"
 // card, README "Quick start"; the product and its epilogue are this library's.)
 //
-// Two kernels, by the number of rows T:
+// Three kernels, by the number of rows T and tiles:
 //   few rows: bound by the packed bytes.  Exact bf16 levels on 16x16x32 ops,
 //     each 32-group's partial sum multiplied by its fp16 scale in fp32, K
 //     split over the waves of a block.  One launch.
+//   some rows: too few tiles to fill the chip, bound by latency.  The operands
+//     of the next kernel, K split over blocks, their fp32 partial results
+//     joined by a second launch with the epilogue.
 //   many rows: bound by the matrix cores.  The scale goes into an fp16
 //     operand, so that one 32x32x16 op follows another over the whole of K,
 //     and the rows are turned to fp16 on their way into LDS.
@@ -17,6 +20,7 @@
 
 #include "device_common.h"
 #include "moe_internal.h"
+#include "topk_common.h"
 
 namespace bqmoe {
 
@@ -70,6 +74,32 @@ __device__ __forceinline__ void finish(const LinArgs& A, float v, int t, int n) 
   if (A.mul) v *= bf16_to_f32(A.mul[(int64_t)t * A.ldm + n]);
   if (A.res) v += bf16_to_f32(A.res[(int64_t)t * A.ldr + n]);
   A.out[(int64_t)t * A.ldo + n] = (uint16_t)f32_to_bf16(v);
+}
+
+// Eight consecutive columns at once (16-byte loads and stores).
+__device__ __forceinline__ void finish8(const LinArgs& A, float (&v)[8], int t, int n) {
+  if (A.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += A.bias[n + j];
+  }
+  for_act(A.act, [&](auto ac) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate<decltype(ac)::value>(v[j]);
+  });
+  if (A.mul) {
+    const u32x4 m = *reinterpret_cast<const u32x4*>(A.mul + (int64_t)t * A.ldm + n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+  }
+  if (A.res) {
+    const u32x4 m = *reinterpret_cast<const u32x4*>(A.res + (int64_t)t * A.ldr + n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+  }
+  u32x4 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
+  *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
 }
 
 // --------------------------------------------------------------- few rows
@@ -640,8 +670,231 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
                       (col * W + wave) * CT * 32);
 }
 
+// --------------------------------------------------------------- some rows
+// Block: 32 NRT rows x 128 columns (4 waves of 32) and a run of k-chunks of
+// four k-blocks.  A chunk is loaded as a whole (every load of it in flight at
+// once, the next chunk's while this one is multiplied), so its rows' and
+// columns' largest values are known before anything is converted: each gets
+// its power of two, and the chunk's product is brought back to scale as it is
+// added to the block's sum.
+// part: where K is split, the partial sums [split][T][N].
+constexpr int kSomeKb = 4;
+template <int Q, int NRT>
+__global__ __launch_bounds__(256, 2) void k_lin_some(LinArgs A, OperandK kk, int T, int row_tiles,
+                                                     int ncol, int run, float* __restrict__ part) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t sbuf[];  // kSomeKb stages
+  constexpr int R = 32 * NRT, kStage = R * 256, kCh = R / 16;
+  constexpr bool Q3 = Q == MOE_Q_INT3;
+  __shared__ __attribute__((aligned(16))) float srow[R];
+  const int tiles = row_tiles * ncol, split = blockIdx.x / tiles, item = blockIdx.x % tiles;
+  const int tile = item / ncol, col = item % ncol;
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, hl = lane >> 5, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int K = A.K, S = K / 128, NT = A.N / 16;
+  const int row0 = tile * R, n0 = col * 128 + 32 * wave;
+  const int c0 = split * run, c1 = min((S + kSomeKb - 1) / kSomeKb, c0 + run);
+  const uint16_t* const xrow = A.x + (int64_t)row0 * A.ldx;
+  uint32_t xo[kCh];
+#pragma unroll
+  for (int i = 0; i < kCh; ++i)
+    xo[i] = (uint32_t)min(4 * (kCh * wave + i) + (lane >> 4), T - 1 - row0) *
+                (uint32_t)(2 * A.ldx) + (lane & 15) * 16;
+  const uint32_t la = (uint32_t)(l32 * 256) | ((uint32_t)(hl ^ (l32 & 15)) << 4);
+  OperandK k = kk;
+  k.b2 = lane_copy(kk.b2);
+  k.b4 = lane_copy(kk.b4);
+  k.b6 = lane_copy(kk.b6);
+  const uint32_t nt = (uint32_t)min((n0 >> 4) + (l32 >> 4), NT - 1);
+  const uint32_t wo = nt * S * 512 + (16 * hl + r) * 8;
+  const uint32_t po = (uint32_t)A.plane1 + nt * S * 256 + (16 * hl + r) * 4;
+  const uint32_t so = (uint32_t)A.scales + nt * S * 128 + r * 8;
+
+  u32x4 xv[kSomeKb][kCh];
+  u32x2 w[kSomeKb][2], sc[kSomeKb];
+  uint32_t w1[kSomeKb][2];
+  // k-blocks past the end repeat the last one (loaded, not multiplied)
+  auto load = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kSomeKb; ++u) {
+      const int kb = min(c * kSomeKb + u, S - 1);
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) xv[u][i] = load_b128(xrow, (int)xo[i], kb * 256);
+    }
+  };
+  auto loadw = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kSomeKb; ++u) {
+      const int kb = min(c * kSomeKb + u, S - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[u][h] = load_b64(A.w, (int)wo, kb * 512 + 256 * h);
+        if (Q3) w1[u][h] = load_b32(A.w, (int)po, kb * 256 + 128 * h);
+      }
+      sc[u] = load_b64(A.w, (int)so, kb * 128);
+    }
+  };
+  f32x16 sum[NRT][1], acc[NRT];
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[rt][0][i] = 0.f;
+  loadw(c0);
+  load(c0);
+  for (int c = c0; c < c1; ++c) {
+    // rows: 2^e brings the largest value to [2^14, 2^15) (16 lanes hold a row)
+    float fac[kCh];
+    __syncthreads();  // the last chunk's rows are read
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int u = 0; u < kSomeKb; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = pk_max_u16(m, xv[u][i][j] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      m = max(m, dpp_u32<0xB1>(m));
+      m = max(m, dpp_u32<0x4E>(m));
+      m = max(m, dpp_u32<0x141>(m));
+      m = max(m, dpp_u32<0x140>(m));
+      const int e = min(114, max(-100, (int)(m >> 7) - 127 - 14));
+      fac[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+      const int row = 4 * (kCh * wave + i) + (lane >> 4);
+      if ((lane & 15) == 0) srow[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int u = 0; u < kSomeKb; ++u) {
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(xv[u][i][j] << 16) * fac[i],
+                                                   __uint_as_float(xv[u][i][j] & 0xFFFF0000u) *
+                                                       fac[i]));
+        *reinterpret_cast<u32x4*>(sbuf + u * kStage + row * 256 +
+                                  (((lane & 15) ^ (row & 15)) << 4)) = o;
+      }
+    }
+    // the column: 2^f brings the largest scale to [2^7, 2^8), f at most 15
+    uint32_t cm = 0;
+#pragma unroll
+    for (int u = 0; u < kSomeKb; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) cm = pk_max_u16(cm, sc[u][i] & 0x7FFF7FFFu);
+    cm = max(cm & 0xFFFFu, cm >> 16);
+    const int f = cm == 0u || cm >= 0x7C00u ? 0 : min(15, 7 - ((int)(cm >> 10) - 15));
+    const uint32_t fh = (uint32_t)(f + 15) << 10, f2 = fh | (fh << 16);
+    const float cs = __uint_as_float((uint32_t)(127 - f) << 23) / kFac<Q>;
+    __syncthreads();
+    if (c + 1 < c1) load(c + 1);
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[rt][i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kSomeKb; ++u)
+      if (c * kSomeKb + u < S) {
+        auto sub = [&](auto qc) __attribute__((always_inline)) {
+          constexpr int q = decltype(qc)::value, GB = q >> 1, h = q & 1;
+          const uint32_t sw = sc[u][GB >> 1];
+          const f16x2 sp = __builtin_bit_cast(f16x2, sw) * __builtin_bit_cast(f16x2, f2);
+          const u32x4 o = weights_f16<Q, GB>(w[u][h][GB >> 1], Q3 ? w1[u][h] : 0u, sp, k);
+          const uint8_t* p = sbuf + u * kStage + (la ^ (uint32_t)((2 * q) << 4));
+#pragma unroll
+          for (int rt = 0; rt < NRT; ++rt)
+            acc[rt] = mfma_lin(*reinterpret_cast<const u32x4*>(p + rt * 8192), o, acc[rt]);
+        };
+        sub(std::integral_constant<int, 0>{});
+        sub(std::integral_constant<int, 1>{});
+        sub(std::integral_constant<int, 2>{});
+        sub(std::integral_constant<int, 3>{});
+        sub(std::integral_constant<int, 4>{});
+        sub(std::integral_constant<int, 5>{});
+        sub(std::integral_constant<int, 6>{});
+        sub(std::integral_constant<int, 7>{});
+      }
+    if (c + 1 < c1) loadw(c + 1);
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 rs = *reinterpret_cast<const f32x4*>(srow + rt * 32 + 8 * j + 4 * hl);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          sum[rt][0][4 * j + i] = fmaf(acc[rt][4 * j + i] * cs, rs[i], sum[rt][0][4 * j + i]);
+      }
+  }
+  if (part) {
+    const int n = n0 + l32;
+    float* o = part + ((size_t)split * T + row0) * A.N + n;
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int m = rt * 32 + 8 * (i >> 2) + 4 * hl + (i & 3);
+        if (row0 + m < T && n < A.N) o[(size_t)m * A.N] = sum[rt][0][i];
+      }
+    return;
+  }
+  __syncthreads();
+  if (tid < R) srow[tid] = 1.f;
+  __syncthreads();
+  const float one[1] = {1.f};
+  store_tile<NRT, 1>(A, sum, 1.f, srow, one, sbuf + wave * kTurnBytes<1>, T, row0, n0);
+}
+
+// Joins the partial sums, in the order of the splits, and finishes.
+__global__ __launch_bounds__(256) void k_lin_join(LinArgs A, int T, int splits,
+                                                  const float* __restrict__ part) {
+  const int per_row = A.N / 8;
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (long)T * per_row) return;
+  const int t = (int)(i / per_row), n = (int)(i % per_row) * 8;
+  const float* p = part + (size_t)t * A.N + n;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s, p += (size_t)T * A.N) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] += a[j];
+      v[4 + j] += b[j];
+    }
+  }
+  finish8(A, v, t, n);
+}
+
 // ------------------------------------------------------------------ launch
-size_t lin_ws_bytes(int, int, int) { return 256; }
+// Which kernel, and how K is split (run chunks a block) for some rows.
+struct LinPlan {
+  enum { kFew, kSome, kMany } kind;
+  int rows, tiles, ncol, run, splits;
+};
+static LinPlan lin_plan(int K, int N, int T) {
+  LinPlan p{};
+  if (T <= kLinFewRows) {
+    p.kind = LinPlan::kFew;
+    return p;
+  }
+  if ((long)((T + 127) / 128) * ((N + 511) / 512) >= 192) {
+    p.kind = LinPlan::kMany;
+    return p;
+  }
+  p.kind = LinPlan::kSome;
+  p.rows = T <= 32 ? 32 : 64;
+  p.tiles = (T + p.rows - 1) / p.rows;
+  p.ncol = (N + 127) / 128;
+  const int chunks = (K / 128 + kSomeKb - 1) / kSomeKb;
+  const long want = 512 / ((long)p.tiles * p.ncol);
+  p.splits = want < 1 ? 1 : want < chunks ? (int)want : chunks;
+  p.run = (chunks + p.splits - 1) / p.splits;
+  p.splits = (chunks + p.run - 1) / p.run;
+  return p;
+}
+
+size_t lin_ws_bytes(int K, int N, int T) {
+  const LinPlan p = lin_plan(K, N, T);
+  if (p.kind != LinPlan::kSome || p.splits == 1) return 256;
+  return ((size_t)p.splits * T * N * 4 + 255) & ~size_t(255);
+}
 
 template <bool Q3>
 static void few(const LinArgs& A, int T, hipStream_t s) {
@@ -663,12 +916,8 @@ static void few(const LinArgs& A, int T, hipStream_t s) {
     BQ_LF(1, 1, 4);
   else if (T <= 8)
     BQ_LF(1, 2, 4);
-  else if (T <= 16)
-    BQ_LF(1, 4, 4);
-  else if (T <= 32)
-    BQ_LF(2, 4, 2);
   else
-    BQ_LF(4, 4, 1);
+    BQ_LF(1, 4, 4);
 #undef BQ_LF
 }
 
@@ -688,7 +937,7 @@ static int gemm(const LinArgs& A, const OperandK& k, int T, hipStream_t s) {
 }
 
 template <int Q>
-static int many(const LinArgs& A, int T, hipStream_t s) {
+static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
   // -(base + offset) * fac for the bases 256, 64, 16
   OperandK k = {0x000C000Cu, 0x00300030u, 0x00C000C0u, 0x5C005C00u, 0x54005400u, 0x4C004C00u,
                 0, 0, 0};
@@ -702,12 +951,25 @@ static int many(const LinArgs& A, int T, hipStream_t s) {
   k.o2 = pair(-(256.f + off) * fac);
   k.o4 = pair(-(64.f + off) * fac);
   k.o6 = pair(-(16.f + off) * fac);
-  const long blocks = (long)((T + 127) / 128) * ((A.N + 511) / 512);
-  if (blocks >= 192) return gemm<Q, 4, 8, 2>(A, k, T, s);
-  return gemm<Q, 2, 4, 1>(A, k, T, s);
+  const LinPlan p = lin_plan(A.K, A.N, T);
+  if (p.kind == LinPlan::kMany) return gemm<Q, 4, 8, 2>(A, k, T, s);
+  float* part = p.splits > 1 ? (float*)ws : nullptr;
+  const dim3 g((unsigned)(p.tiles * p.ncol * p.splits));
+  constexpr int stages = kSomeKb * 256, turn = 4 * kTurnBytes<1>;
+  if (p.rows == 32)
+    hipLaunchKernelGGL((k_lin_some<Q, 1>), g, dim3(256), 32 * stages, s, A, k, T, p.tiles, p.ncol,
+                       p.run, part);
+  else
+    hipLaunchKernelGGL((k_lin_some<Q, 2>), g, dim3(256), 64 * stages, s, A, k, T, p.tiles, p.ncol,
+                       p.run, part);
+  static_assert(turn <= 32 * stages, "turning area");
+  if (part)
+    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)(((long)T * (A.N / 8) + 255) / 256)), dim3(256),
+                       0, s, A, T, p.splits, part);
+  return (int)hipGetLastError();
 }
 
-int launch_linear(const LinArgs& A, int T, void* stream) {
+int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream) {
   hipStream_t s = (hipStream_t)stream;
   if (T <= kLinFewRows) {
     if (A.q == MOE_Q_INT3)
@@ -716,9 +978,9 @@ int launch_linear(const LinArgs& A, int T, void* stream) {
       few<false>(A, T, s);
     return (int)hipGetLastError();
   }
-  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, T, s);
-  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, T, s);
-  return many<MOE_Q_INT3>(A, T, s);
+  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, T, ws, s);
+  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, T, ws, s);
+  return many<MOE_Q_INT3>(A, T, ws, s);
 }
 
 }  // namespace bqmoe

@@ -335,7 +335,7 @@ moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_scoring* S, 
  *                     act( sum_k x[t][k] * W[k][n] [+ bias[n]] ) )
  *
  * Sums, bias, activation, product and residual are fp32, rounded to bf16
- * once.  For up to 64 rows the weights enter the product exactly; beyond,
+ * once.  For up to 16 rows the weights enter the product exactly; beyond,
  * 2- and 3-bit weights s * (u - offset) are rounded to fp16's 11 significant
  * bits (at most 2^-12 of a weight; ternary ones are exact), and values of x
  * below 2^-31 of their row's largest may lose bits.

@@ -197,7 +197,7 @@ def _bound(c):
     """How far a result may be from the 64-bit one, value by value.
 
     Before the activation, with A = sum |x| |s| and S = sum |x W| + |bias|:
-    * up to 64 rows, levels on a base: two 32-term sums of magnitude at most
+    * up to 16 rows, levels on a base: two 32-term sums of magnitude at most
       1.25 sum |x| each per group, every term rounded once in each of at most
       34 steps (2^-23, whatever the order and rounding mode), times 32 s:
       32 * 2.5 * 34 * 2^-23 A; then K/32 + 10 steps over the groups, 2^-23 S;
@@ -210,7 +210,7 @@ def _bound(c):
     """
     x, w = np.abs(c.x.double().numpy()), np.abs(c.weights())
     S = x @ w.T + (0 if c.bias is None else np.abs(c.bias))
-    if c.T <= 64:
+    if c.T <= 16:
         A = x @ np.repeat(np.abs(c.scales.astype(np.float64)), 32, axis=1).T
         e = 32 * 2.5 * 34 * 2.0 ** -23 * A + (c.K / 32 + 10) * 2.0 ** -23 * S
     else:
@@ -246,7 +246,10 @@ def _check(c, got):
         assert rel <= 2.0 ** -8 + slack
 
 
+# The three kernels: up to 16 rows; tiles of 32 or 64 rows with K split or not; tiles of 128
+# rows (from 192 tiles of 128 x 512 on).
 ROWS = [1, 2, 4, 5, 8, 9, 16, 17, 31, 33, 64, 65, 100, 128, 129, 300]
+MANY = (3000, 4096)  # rows and columns that take the last one
 
 
 @pytest.mark.gpu
@@ -264,7 +267,8 @@ def test_exact_values(T, q, K, N):
 @pytest.mark.gpu
 @pytest.mark.parametrize("q", [1, 2, 3])
 @pytest.mark.parametrize("T,K,N", [(1, 4096, 528), (7, 1280, 1024), (64, 2176, 1040),
-                                   (700, 2048, 1552), (2100, 640, 4112), (8200, 256, 2064)])
+                                   (23, 4096, 16), (700, 2048, 1552), (2100, 640, 4112),
+                                   (8200, 256, 2064), (2945, 384, 4080), (3001, 128, 4112)])
 def test_exact_values_at_larger_shapes(q, T, K, N):
     c = Case(T, K, N, q, act="none", bias=True, res=True, exact=True)
     assert torch.equal(c.run(), _bf16(c.reference().astype(np.float32)))
@@ -272,11 +276,14 @@ def test_exact_values_at_larger_shapes(q, T, K, N):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", list(ACTS))
-@pytest.mark.parametrize("T", [3, 40, 90])
-def test_epilogues(act, T):
+@pytest.mark.parametrize("T,K,N", [(3, 512, 160), (40, 640, 160), (90, 2048, 160), (90, 256, 4112),
+                                   (MANY[0], 128, MANY[1])])
+def test_epilogues(act, T, K, N):
     for q, bias, mul, res in ((1, True, False, True), (2, False, True, False),
                               (3, True, True, True)):
-        c = Case(T, 512, 160, q, act, bias, mul, res, pad=8 * (q == 3))
+        if T * N > 1e6 and q != 1 + list(ACTS).index(act) % 3:
+            continue
+        c = Case(T, K, N, q, act, bias, mul, res, pad=8 * (q == 3))
         _check(c, c.run())
 
 
@@ -291,11 +298,12 @@ def test_random_values(T, K, N, q):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [4, 80])
+@pytest.mark.parametrize("T,K,N", [(4, 512, 96), (80, 512, 96), (20, 2048, 96), (70, 1152, 4096),
+                                   (MANY[0], 256, MANY[1])])
 @pytest.mark.parametrize("q", [1, 2, 3])
-def test_very_small_and_very_large_scales_and_rows(T, q):
+def test_very_small_and_very_large_scales_and_rows(T, K, N, q):
     for scale in (2.0 ** -22, 2.0 ** -14, 9000.0):
-        c = Case(T, 512, 96, q, scale=scale)
+        c = Case(T, K, N, q, scale=scale)
         c.scales = np.minimum(c.scales, np.float16(60000))
         x = c.x.double().numpy()
         x[0] *= 2.0 ** 60
@@ -304,15 +312,15 @@ def test_very_small_and_very_large_scales_and_rows(T, q):
         x[3, ::3] *= 2.0 ** -12
         c.x = _bf16(x)
         g, ref, e = c.run().double().numpy(), c.reference(), _bound(c)
-        # a scale below 2^-24 * 2^13 of ... keeps its bits: columns are scaled by a power of two
         assert (np.abs(g - ref) <= e).all(), (np.abs(g - ref) / e).max()
         assert (g[2] == 0).all()
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [5, 70])
-def test_infinities_and_nan_stay_in_their_rows(T):
-    c = Case(T, 256, 64, 2)
+@pytest.mark.parametrize("T,K,N", [(5, 256, 64), (70, 256, 64), (70, 2048, 64),
+                                   (MANY[0], 256, MANY[1])])
+def test_infinities_and_nan_stay_in_their_rows(T, K, N):
+    c = Case(T, K, N, 2)
     clean = c.run()
     x = c.x.clone()
     x[1, 7] = float("inf")
@@ -325,9 +333,10 @@ def test_infinities_and_nan_stay_in_their_rows(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [8, 200])
-def test_in_place_on_the_residual_stream_and_deterministic(T):
-    c = Case(T, 512, 256, 3, res=True)
+@pytest.mark.parametrize("T,K,N", [(8, 512, 256), (200, 512, 256), (200, 1152, 256),
+                                   (MANY[0], 256, MANY[1])])
+def test_in_place_on_the_residual_stream_and_deterministic(T, K, N):
+    c = Case(T, K, N, 3, res=True)
     a, b = c.run(), c.run(in_place=True)
     assert torch.equal(a, b)
 
@@ -336,7 +345,7 @@ def test_in_place_on_the_residual_stream_and_deterministic(T):
 @pytest.mark.parametrize("T", [1, 33, 150])
 def test_captured_into_a_graph(T):
     c = Case(T, 640, 144, 2, act="gelu_tanh", bias=True)
-    lin, ws = c.linear(), None
+    lin = c.linear()
     ws = bq.alloc_linear_workspace(lin, T)
     x = torch.zeros(T, c.K, dtype=torch.bfloat16, device=DEV)
     out = torch.zeros(T, c.N, dtype=torch.bfloat16, device=DEV)
