@@ -157,8 +157,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -366,11 +366,15 @@ def moe_forward_prefill_scored(layer: Layer, scoring: Scoring, x, T: int, flags:
 
 
 # ------------------------------------------------------ dense product
-@dataclass
 class Linear:
     """A moe_linear plus the tensors it points into (kept alive here)."""
-    c: moe_linear
-    tensors: tuple
+
+    def __init__(self, c: moe_linear, tensors: tuple = ()):
+        self.c, self.tensors, self.ref = c, tensors, ctypes.byref(c)
+        on = {t.get_device() for t in tensors if isinstance(t, torch.Tensor)}
+        if len(on) > 1:
+            raise MoeError(MOE_ERR_INVALID_ARG, "make_linear: w and bias are on different devices")
+        self.device = on.pop() if on else -1  # -1: addresses, not tensors
 
 
 def make_linear(K: int, N: int, qtype: int, w, bias=None, act: int = MOE_ACT_NONE) -> Linear:
@@ -395,15 +399,15 @@ def alloc_linear_workspace(linear: Linear, T: int, device="cuda") -> torch.Tenso
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _rows(t, width: int, T: int, device, what: str):
-    """(address, row stride) of a [T][width] operand of 16-bit values on `device`."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or t.element_size() != 2 or t.shape[0] < T or t.shape[1] != width or \
-            (t.stride(1) != 1 and width > 1) or t.device != device or not t.is_cuda:
+def _rows(t: torch.Tensor, width: int, T: int, dev: int, what: str):
+    """(address, row stride) of a [T][width] operand of 16-bit values on GPU `dev`."""
+    rows, cols = t.shape if t.dim() == 2 else (-1, -1)
+    stride, one = t.stride() if rows >= 0 else (0, 0)
+    if cols != width or rows < T or one != 1 or t.itemsize != 2 or not t.is_cuda or \
+            t.get_device() != dev:
         raise MoeError(MOE_ERR_INVALID_ARG, f"moe_linear_forward: {what} must be at least {T} rows "
-                       f"of {width} adjacent 16-bit values on {device}")
-    return t.data_ptr(), t.stride(0) if T > 1 else -(-width // 8) * 8
+                       f"of {width} adjacent 16-bit values on GPU {dev}")
+    return t.data_ptr(), stride if T > 1 else (width + 7) // 8 * 8
 
 
 def moe_linear_forward(linear: Linear, x: torch.Tensor, T: int, out: torch.Tensor,
@@ -412,21 +416,21 @@ def moe_linear_forward(linear: Linear, x: torch.Tensor, T: int, out: torch.Tenso
     """out = bf16([residual +] [mul *] act(x.W + bias)) over the first T rows of the 2-d device
     tensors x [.][K], mul, residual and out [.][N] (bf16 values or their bit patterns; rows may be
     any multiple of 8 values apart).  Runs on x's device, on its current stream by default."""
-    c, dev = linear.c, x.device
-    if x.is_cuda and dev.index != torch.cuda.current_device():
+    c, dev = linear.c, x.get_device()
+    if dev >= 0 and dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return moe_linear_forward(linear, x, T, out, ws, mul, residual, stream)
     xp, xs = _rows(x, c.K, T, dev, "x")
-    mp, ms = _rows(mul, c.N, T, dev, "mul")
-    rp, rs = _rows(residual, c.N, T, dev, "residual")
     op, os_ = _rows(out, c.N, T, dev, "out")
-    for t in (*linear.tensors, ws):
-        if isinstance(t, torch.Tensor) and t.device != dev:
-            raise MoeError(MOE_ERR_INVALID_ARG, f"moe_linear_forward: a tensor is not on {dev}")
-    st = load().moe_linear_forward(ctypes.byref(c), xp, xs, T, mp, ms, rp, rs, op, os_, _ptr(ws),
-                                   0 if ws is None else ws.numel() * ws.element_size(),
+    mp, ms = _rows(mul, c.N, T, dev, "mul") if mul is not None else (None, 0)
+    rp, rs = _rows(residual, c.N, T, dev, "residual") if residual is not None else (None, 0)
+    wsp, wsn = (ws.data_ptr(), ws.nbytes) if ws is not None else (None, 0)
+    if linear.device >= 0 and linear.device != dev or ws is not None and ws.get_device() != dev:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"moe_linear_forward: not every tensor is on GPU {dev}")
+    st = load().moe_linear_forward(linear.ref, xp, xs, T, mp, ms, rp, rs, op, os_, wsp, wsn,
                                    _stream(stream))
-    _check(st, "moe_linear_forward")
+    if st != MOE_OK:
+        raise MoeError(st, "moe_linear_forward")
 
 
 def moe_abi_version() -> int:

@@ -17,6 +17,7 @@
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "device_common.h"
 #include "moe_internal.h"
@@ -76,30 +77,27 @@ __device__ __forceinline__ void finish(const LinArgs& A, float v, int t, int n) 
   A.out[(int64_t)t * A.ldo + n] = (uint16_t)f32_to_bf16(v);
 }
 
-// Eight consecutive columns at once (16-byte loads and stores).
-__device__ __forceinline__ void finish8(const LinArgs& A, float (&v)[8], int t, int n) {
-  if (A.bias) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += A.bias[n + j];
-  }
+// Four consecutive columns at once (8-byte loads and stores).
+__device__ __forceinline__ void finish4(const LinArgs& A, f32x4 v, int t, int n) {
+  if (A.bias) v += *reinterpret_cast<const f32x4*>(A.bias + n);
   for_act(A.act, [&](auto ac) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate<decltype(ac)::value>(v[j]);
+    for (int j = 0; j < 4; ++j) v[j] = activate<decltype(ac)::value>(v[j]);
   });
   if (A.mul) {
-    const u32x4 m = *reinterpret_cast<const u32x4*>(A.mul + (int64_t)t * A.ldm + n);
+    const u32x2 m = *reinterpret_cast<const u32x2*>(A.mul + (int64_t)t * A.ldm + n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+    for (int j = 0; j < 4; ++j) v[j] *= bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
   }
   if (A.res) {
-    const u32x4 m = *reinterpret_cast<const u32x4*>(A.res + (int64_t)t * A.ldr + n);
+    const u32x2 m = *reinterpret_cast<const u32x2*>(A.res + (int64_t)t * A.ldr + n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+    for (int j = 0; j < 4; ++j) v[j] += bf16_to_f32((m[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
   }
-  u32x4 o;
+  u32x2 o;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
-  *reinterpret_cast<u32x4*>(A.out + (int64_t)t * A.ldo + n) = o;
+  for (int j = 0; j < 2; ++j) o[j] = f32_to_bf16(v[2 * j]) | (f32_to_bf16(v[2 * j + 1]) << 16);
+  *reinterpret_cast<u32x2*>(A.out + (int64_t)t * A.ldo + n) = o;
 }
 
 // --------------------------------------------------------------- few rows
@@ -300,6 +298,16 @@ __device__ __forceinline__ uint32_t load_b32(const void* base, int off, int soff
   return __builtin_amdgcn_raw_buffer_load_b32(rsrc_of(base), off, soff, 0);
 }
 
+// f(integral constants 0 .. N-1)
+template <int... I, typename F>
+__device__ __forceinline__ void for_ints_impl(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void for_ints(F f) {
+  for_ints_impl(std::make_integer_sequence<int, N>{}, f);
+}
+
 __device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
@@ -434,7 +442,9 @@ template <int Q, int NRT, int W, int CT>
 __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, int T,
                                                         int row_tiles, int ncol) {
   extern __shared__ __attribute__((aligned(16))) uint8_t sbuf[];
-  constexpr int R = 32 * NRT, kStage = R * 256, kCh = R / (4 * W);
+  // small tiles have registers to spare and short steps: their rows are loaded
+  // two steps ahead of their conversion, their words a whole step
+  constexpr int R = 32 * NRT, kStage = R * 256, kCh = R / (4 * W), kDeep = NRT * CT <= 2 ? 2 : 1;
   static_assert(R % (4 * W) == 0 && kCh <= 8, "row split");
   constexpr bool Q3 = Q == MOE_Q_INT3;
   __shared__ __attribute__((aligned(16))) float srow[R];
@@ -486,12 +496,12 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
     u32x2 w[CT][2], s[CT];
     uint32_t w1[CT][2];
   };
-  u32x4 xv[kCh];               // bf16 rows of the step after the next
+  u32x4 xv[kDeep][kCh];        // bf16 rows of the steps after this one
   float rmax[kCh], rfac[kCh];  // the rows' largest |x| so far, 2^-e of pass 2
   uint32_t cmax[CT], cm[CT];   // the column's largest |scale| (two halves), 2^f twice
   f32x16 acc[NRT][CT];
-  auto loadx = [&](int s, int i) __attribute__((always_inline)) {
-    xv[i] = load_b128(xrow, (int)xo[i], min(s, S - 1) * 256);
+  auto loadx = [&](int s, int i, u32x4 (&x)[kCh]) __attribute__((always_inline)) {
+    x[i] = load_b128(xrow, (int)xo[i], min(s, S - 1) * 256);
   };
   auto loadb = [&](int s, Words& b) __attribute__((always_inline)) {
 #pragma unroll
@@ -529,12 +539,12 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
         o[ct] = weights_f16<Q, GB>(b.w[ct][h][GB >> 1], Q3 ? b.w1[ct][h] : 0u, sp, k);
       }
     };
-    // chunk i of xv as fp16 into LDS stage st
-    auto convert = [&](int i, int st) __attribute__((always_inline)) {
+    // chunk i of x as fp16 into LDS stage st
+    auto convert = [&](int i, int st, const u32x4 (&x)[kCh]) __attribute__((always_inline)) {
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float a = __uint_as_float(xv[i][j] << 16), b = __uint_as_float(xv[i][j] & 0xFFFF0000u);
+        float a = __uint_as_float(x[i][j] << 16), b = __uint_as_float(x[i][j] & 0xFFFF0000u);
         if (SC) {
           a *= rfac[i];
           b *= rfac[i];
@@ -549,8 +559,8 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
     // sub-step q of a step (group q/2, k-half q%2): the next sub-step's rows
     // are read, its weights built and a part of the next step's rows
     // converted while this one's matrix-core ops run
-    auto sub = [&](auto qc, int s, uint32_t at, const Words& b, const Words& bn, u32x4 (&a0)[NRT],
-                   u32x4 (&a1)[NRT], u32x4 (&o0)[CT], u32x4 (&o1)[CT])
+    auto sub = [&](auto qc, int s, uint32_t at, const Words& b, const Words& bn, u32x4 (&x)[kCh],
+                   u32x4 (&a0)[NRT], u32x4 (&a1)[NRT], u32x4 (&o0)[CT], u32x4 (&o1)[CT])
         __attribute__((always_inline)) {
       constexpr int q = decltype(qc)::value;
       if constexpr (q < 7) loada(at, q + 1, a1);
@@ -558,7 +568,7 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
         build(std::integral_constant<int, q + 1>{}, b, o1);
       else
         build(std::integral_constant<int, 0>{}, bn, o1);
-      if constexpr (q < kCh) convert(q, (s + 1) & 1);
+      if constexpr (q < kCh) convert(q, (s + 1) & 1, x);
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
@@ -570,20 +580,26 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (q < kCh) loadx(s + 2, q);
+      if constexpr (q < kCh) loadx(s + 1 + kDeep, q, x);
       __builtin_amdgcn_sched_barrier(0);
     };
     Words wa, wb;
     u32x4 a0[NRT], a1[NRT], o0[CT], o1[CT];
+    // step s converts x of step s + 1, from xv[s % kDeep]
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) loadx(0, i);
+    for (int i = 0; i < kCh; ++i) loadx(0, i, xv[kDeep - 1]);
     loadb(0, wa);
+    if (kDeep == 2) {
+      loadb(min(1, S - 1), wb);
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) convert(i, 0);
+      for (int i = 0; i < kCh; ++i) loadx(1, i, xv[0]);
+    }
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) loadx(1, i);
+    for (int i = 0; i < kCh; ++i) convert(i, 0, xv[kDeep - 1]);
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) loadx(kDeep, i, xv[kDeep - 1]);
     build(std::integral_constant<int, 0>{}, wa, o0);
-    auto step = [&](int s, const Words& b, Words& bn) __attribute__((always_inline)) {
+    auto step = [&](int s, Words& b, Words& bn, u32x4 (&x)[kCh]) __attribute__((always_inline)) {
       // step s's rows are in LDS for every wave, and every wave is done with
       // the stage that step s + 1's overwrite
       __builtin_amdgcn_s_waitcnt(wait_vm_lgkm(63, 0));
@@ -598,25 +614,27 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
           for (int i = 0; i < 2; ++i) cmax[ct] = pk_max_u16(cmax[ct], b.s[ct][i] & 0x7FFF7FFFu);
       }
       __builtin_amdgcn_sched_barrier(0);
-      sub(std::integral_constant<int, 0>{}, s, at, b, bn, a0, a1, o0, o1);
-      sub(std::integral_constant<int, 1>{}, s, at, b, bn, a1, a0, o1, o0);
-      sub(std::integral_constant<int, 2>{}, s, at, b, bn, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 0>{}, s, at, b, bn, x, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 1>{}, s, at, b, bn, x, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 2>{}, s, at, b, bn, x, a0, a1, o0, o1);
       // the next step's words, where half of this one's are done with (past
       // the last step they repeat it, so that there is no branch)
-      loadb(min(s + 1, S - 1), bn);
+      if (kDeep == 1) loadb(min(s + 1, S - 1), bn);
       __builtin_amdgcn_sched_barrier(0);
-      sub(std::integral_constant<int, 3>{}, s, at, b, bn, a1, a0, o1, o0);
-      sub(std::integral_constant<int, 4>{}, s, at, b, bn, a0, a1, o0, o1);
-      sub(std::integral_constant<int, 5>{}, s, at, b, bn, a1, a0, o1, o0);
-      sub(std::integral_constant<int, 6>{}, s, at, b, bn, a0, a1, o0, o1);
-      sub(std::integral_constant<int, 7>{}, s, at, b, bn, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 3>{}, s, at, b, bn, x, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 4>{}, s, at, b, bn, x, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 5>{}, s, at, b, bn, x, a1, a0, o1, o0);
+      sub(std::integral_constant<int, 6>{}, s, at, b, bn, x, a0, a1, o0, o1);
+      sub(std::integral_constant<int, 7>{}, s, at, b, bn, x, a1, a0, o1, o0);
+      if (kDeep == 2) loadb(min(s + 2, S - 1), b);
+      __builtin_amdgcn_sched_barrier(0);
     };
     int s = 0;
     for (; s + 1 < S; s += 2) {
-      step(s, wa, wb);
-      step(s + 1, wb, wa);
+      step(s, wa, wb, xv[0]);
+      step(s + 1, wb, wa, xv[kDeep - 1]);
     }
-    if (s < S) step(s, wa, wb);
+    if (s < S) step(s, wa, wb, xv[0]);
     __syncthreads();  // the stages are free
   };
 
@@ -712,7 +730,7 @@ __global__ __launch_bounds__(256, 2) void k_lin_some(LinArgs A, OperandK kk, int
   u32x4 xv[kSomeKb][kCh];
   u32x2 w[kSomeKb][2], sc[kSomeKb];
   uint32_t w1[kSomeKb][2];
-  // k-blocks past the end repeat the last one (loaded, not multiplied)
+  // (k-blocks past the end repeat the last one's loads and count as zero rows)
   auto load = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < kSomeKb; ++u) {
@@ -747,6 +765,9 @@ __global__ __launch_bounds__(256, 2) void k_lin_some(LinArgs A, OperandK kk, int
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
       uint32_t m = 0;
+#pragma unroll
+      for (int u = 1; u < kSomeKb; ++u)
+        if (c * kSomeKb + u >= S) xv[u][i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int u = 0; u < kSomeKb; ++u)
 #pragma unroll
@@ -789,28 +810,41 @@ __global__ __launch_bounds__(256, 2) void k_lin_some(LinArgs A, OperandK kk, int
     for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[rt][i] = 0.f;
+    // 32 sub-steps of 16 k: the next one's rows are read and its weights built
+    // while this one's matrix-core ops run
+    auto rows = [&](auto qc, u32x4 (&a)[NRT]) __attribute__((always_inline)) {
+      constexpr int u = decltype(qc)::value >> 3, q = decltype(qc)::value & 7;
+      const uint8_t* p = sbuf + u * kStage + (la ^ (uint32_t)((2 * q) << 4));
 #pragma unroll
-    for (int u = 0; u < kSomeKb; ++u)
-      if (c * kSomeKb + u < S) {
-        auto sub = [&](auto qc) __attribute__((always_inline)) {
-          constexpr int q = decltype(qc)::value, GB = q >> 1, h = q & 1;
-          const uint32_t sw = sc[u][GB >> 1];
-          const f16x2 sp = __builtin_bit_cast(f16x2, sw) * __builtin_bit_cast(f16x2, f2);
-          const u32x4 o = weights_f16<Q, GB>(w[u][h][GB >> 1], Q3 ? w1[u][h] : 0u, sp, k);
-          const uint8_t* p = sbuf + u * kStage + (la ^ (uint32_t)((2 * q) << 4));
-#pragma unroll
-          for (int rt = 0; rt < NRT; ++rt)
-            acc[rt] = mfma_lin(*reinterpret_cast<const u32x4*>(p + rt * 8192), o, acc[rt]);
-        };
-        sub(std::integral_constant<int, 0>{});
-        sub(std::integral_constant<int, 1>{});
-        sub(std::integral_constant<int, 2>{});
-        sub(std::integral_constant<int, 3>{});
-        sub(std::integral_constant<int, 4>{});
-        sub(std::integral_constant<int, 5>{});
-        sub(std::integral_constant<int, 6>{});
-        sub(std::integral_constant<int, 7>{});
+      for (int rt = 0; rt < NRT; ++rt) a[rt] = *reinterpret_cast<const u32x4*>(p + rt * 8192);
+    };
+    auto build = [&](auto qc) __attribute__((always_inline)) {
+      constexpr int u = decltype(qc)::value >> 3, q = decltype(qc)::value & 7;
+      constexpr int GB = q >> 1, h = q & 1;
+      const uint32_t sw = sc[u][GB >> 1];
+      const f16x2 sp = __builtin_bit_cast(f16x2, sw) * __builtin_bit_cast(f16x2, f2);
+      return weights_f16<Q, GB>(w[u][h][GB >> 1], Q3 ? w1[u][h] : 0u, sp, k);
+    };
+    u32x4 a[2][NRT], o[2];
+    rows(std::integral_constant<int, 0>{}, a[0]);
+    o[0] = build(std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    for_ints<8 * kSomeKb>([&](auto qc) __attribute__((always_inline)) {
+      constexpr int q = decltype(qc)::value;
+      if constexpr (q + 1 < 8 * kSomeKb) {
+        rows(std::integral_constant<int, q + 1>{}, a[(q + 1) & 1]);
+        o[(q + 1) & 1] = build(std::integral_constant<int, q + 1>{});
       }
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt) acc[rt] = mfma_lin(a[q & 1][rt], o[q & 1], acc[rt]);
+#pragma unroll
+      for (int i = 0; i < NRT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 24 / NRT, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
     if (c + 1 < c1) loadw(c + 1);
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt)
@@ -841,58 +875,107 @@ __global__ __launch_bounds__(256, 2) void k_lin_some(LinArgs A, OperandK kk, int
   store_tile<NRT, 1>(A, sum, 1.f, srow, one, sbuf + wave * kTurnBytes<1>, T, row0, n0);
 }
 
-// Joins the partial sums, in the order of the splits, and finishes.
+// Joins the partial sums, in the order of the splits, and finishes: one
+// thread per four columns, eight splits' loads in flight at once.
 __global__ __launch_bounds__(256) void k_lin_join(LinArgs A, int T, int splits,
                                                   const float* __restrict__ part) {
-  const int per_row = A.N / 8;
+  const int per_row = A.N / 4;
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= (long)T * per_row) return;
-  const int t = (int)(i / per_row), n = (int)(i % per_row) * 8;
+  const int t = (int)(i / per_row), n = (int)(i % per_row) * 4;
   const float* p = part + (size_t)t * A.N + n;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s, p += (size_t)T * A.N) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  const size_t step = (size_t)T * A.N;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    f32x4 v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] += a[j];
-      v[4 + j] += b[j];
-    }
+    for (int s = 0; s < 8; ++s)  // (past the last split: it again, not added)
+      v[s] = *reinterpret_cast<const f32x4*>(p + min(s0 + s, splits - 1) * step);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < splits) sum += v[s];
   }
-  finish8(A, v, t, n);
+  finish4(A, sum, t, n);
 }
 
 // ------------------------------------------------------------------ launch
-// Which kernel, and how K is split (run chunks a block) for some rows.
+// Which kernel takes a call: the one whose time, in us, is the least by these
+// estimates, fitted to sweeps of T = 1 .. 3000 at (K, N) from (512, 8192) to
+// (8192, 1024), S = K / 128 steps and b blocks of each kernel:
+//   few     2.5 + S * 0.24 (T <= 32) or 0.54, more where b exceeds the CUs
+//           (4096 x 4096: 10.3 us at T = 32, 21.5 at 64)
+//   some    3.8 + run * b * 0.0095 (32 rows a tile) or 0.022 (64), and the
+//           second launch (4096 x 2064, T = 77: 13.5 us; the smallest tiles of
+//           the next kernel unsplit 24.6)
+//   tiles   a step takes a latency-bound time while the CUs have a block or
+//           less and grows with the blocks beyond it (4096 x 4096: 32 x 128
+//           22 us at T = 77, 64 x 128 34.5 at 512, 64 x 256 51 at 1000,
+//           128 x 256 77 at 2048, 128 x 512 115 at 3000; each of them up to
+//           twice that one size away)
+// Up to 16 rows are always few (their exact weights).
+struct LinTile {
+  int nrt, waves, ct;        // rows / 32, waves, columns of a wave / 32
+  float floor, base, slope;  // us a step: max(floor, base + slope * b / 256)
+};
+constexpr LinTile kLinTiles[] = {{1, 4, 1, 0.62f, 0.30f, 0.43f},
+                                 {2, 4, 1, 0.80f, 0.33f, 0.68f},
+                                 {2, 8, 1, 0.96f, 0.40f, 1.13f},
+                                 {4, 8, 1, 1.35f, 1.00f, 1.35f},
+                                 {4, 8, 2, 2.45f, 2.30f, 1.60f}};
 struct LinPlan {
-  enum { kFew, kSome, kMany } kind;
-  int rows, tiles, ncol, run, splits;
+  int kind;  // -2 few, -1 some, else the tile's place in kLinTiles
+  int rows, tiles, ncol, run, splits;  // some
 };
 static LinPlan lin_plan(int K, int N, int T) {
-  LinPlan p{};
+  LinPlan best{};
+  best.kind = -2;
+  if (T <= 16) return best;
+  const int S = K / 128;
+  float cost = 1e30f;
   if (T <= kLinFewRows) {
-    p.kind = LinPlan::kFew;
-    return p;
+    const float over = N > 4096 ? (float)N / 4096.f : 1.f;
+    cost = 2.5f + S * (T <= 32 ? 0.24f : 0.54f) * over;
   }
-  if ((long)((T + 127) / 128) * ((N + 511) / 512) >= 192) {
-    p.kind = LinPlan::kMany;
-    return p;
+  {
+    LinPlan p{};
+    p.kind = -1;
+    p.ncol = (N + 127) / 128;
+    const int chunks = (S + kSomeKb - 1) / kSomeKb;
+    // 32-row tiles, three blocks to a CU, where they fit; else 64-row ones, two
+    p.rows = (long)((T + 31) / 32) * p.ncol * chunks <= 768 ? 32 : 64;
+    p.tiles = (T + p.rows - 1) / p.rows;
+    const long want = (p.rows == 32 ? 768 : 512) / ((long)p.tiles * p.ncol);
+    p.splits = want < 1 ? 1 : want < chunks ? (int)want : chunks;
+    p.run = (chunks + p.splits - 1) / p.splits;
+    p.splits = (chunks + p.run - 1) / p.run;
+    const float b = (float)p.tiles * p.ncol * p.splits;
+    float c = 3.8f + p.run * b * (p.rows == 32 ? 0.0095f : 0.022f) + 1.5f * (p.run - 1);
+    if (p.splits > 1) c += 2.5f + (float)p.splits * T * N * 1.0e-6f;
+    if (c < cost && (long)p.tiles * p.ncol * p.splits <= 1 << 20) {
+      cost = c;
+      best = p;
+    }
   }
-  p.kind = LinPlan::kSome;
-  p.rows = T <= 32 ? 32 : 64;
-  p.tiles = (T + p.rows - 1) / p.rows;
-  p.ncol = (N + 127) / 128;
-  const int chunks = (K / 128 + kSomeKb - 1) / kSomeKb;
-  const long want = 512 / ((long)p.tiles * p.ncol);
-  p.splits = want < 1 ? 1 : want < chunks ? (int)want : chunks;
-  p.run = (chunks + p.splits - 1) / p.splits;
-  p.splits = (chunks + p.run - 1) / p.run;
-  return p;
+  for (int i = 0; i < 5; ++i) {
+    const LinTile& v = kLinTiles[i];
+    const long b = (long)((T + 32 * v.nrt - 1) / (32 * v.nrt)) *
+                   ((N + 32 * v.ct * v.waves - 1) / (32 * v.ct * v.waves));
+    // the fullest CU sets the time; the largest tile has one block to a CU at a time
+    const float f = b <= 256 ? (float)b / 256.f : (float)((b + 255) / 256);
+    float step = v.ct == 2 && f > 1.f ? (v.base + v.slope) * f : v.base + v.slope * f;
+    step = step < v.floor ? v.floor : step;
+    const float c = 3.f + S * step;
+    if (c < cost) {
+      cost = c;
+      best.kind = i;
+    }
+  }
+  return best;
 }
 
 size_t lin_ws_bytes(int K, int N, int T) {
   const LinPlan p = lin_plan(K, N, T);
-  if (p.kind != LinPlan::kSome || p.splits == 1) return 256;
+  if (p.kind != -1 || p.splits == 1) return 256;
   return ((size_t)p.splits * T * N * 4 + 255) & ~size_t(255);
 }
 
@@ -916,8 +999,12 @@ static void few(const LinArgs& A, int T, hipStream_t s) {
     BQ_LF(1, 1, 4);
   else if (T <= 8)
     BQ_LF(1, 2, 4);
-  else
+  else if (T <= 16)
     BQ_LF(1, 4, 4);
+  else if (T <= 32)
+    BQ_LF(2, 4, 2);
+  else
+    BQ_LF(4, 4, 1);
 #undef BQ_LF
 }
 
@@ -937,7 +1024,7 @@ static int gemm(const LinArgs& A, const OperandK& k, int T, hipStream_t s) {
 }
 
 template <int Q>
-static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
+static int many(const LinArgs& A, const LinPlan& p, int T, uint8_t* ws, hipStream_t s) {
   // -(base + offset) * fac for the bases 256, 64, 16
   OperandK k = {0x000C000Cu, 0x00300030u, 0x00C000C0u, 0x5C005C00u, 0x54005400u, 0x4C004C00u,
                 0, 0, 0};
@@ -951,8 +1038,13 @@ static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
   k.o2 = pair(-(256.f + off) * fac);
   k.o4 = pair(-(64.f + off) * fac);
   k.o6 = pair(-(16.f + off) * fac);
-  const LinPlan p = lin_plan(A.K, A.N, T);
-  if (p.kind == LinPlan::kMany) return gemm<Q, 4, 8, 2>(A, k, T, s);
+  switch (p.kind) {
+    case 0: return gemm<Q, 1, 4, 1>(A, k, T, s);
+    case 1: return gemm<Q, 2, 4, 1>(A, k, T, s);
+    case 2: return gemm<Q, 2, 8, 1>(A, k, T, s);
+    case 3: return gemm<Q, 4, 8, 1>(A, k, T, s);
+    case 4: return gemm<Q, 4, 8, 2>(A, k, T, s);
+  }
   float* part = p.splits > 1 ? (float*)ws : nullptr;
   const dim3 g((unsigned)(p.tiles * p.ncol * p.splits));
   constexpr int stages = kSomeKb * 256, turn = 4 * kTurnBytes<1>;
@@ -964,23 +1056,24 @@ static int many(const LinArgs& A, int T, uint8_t* ws, hipStream_t s) {
                        p.run, part);
   static_assert(turn <= 32 * stages, "turning area");
   if (part)
-    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)(((long)T * (A.N / 8) + 255) / 256)), dim3(256),
+    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)(((long)T * (A.N / 4) + 255) / 256)), dim3(256),
                        0, s, A, T, p.splits, part);
   return (int)hipGetLastError();
 }
 
 int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  if (T <= kLinFewRows) {
+  const LinPlan p = lin_plan(A.K, A.N, T);
+  if (p.kind == -2) {
     if (A.q == MOE_Q_INT3)
       few<true>(A, T, s);
     else
       few<false>(A, T, s);
     return (int)hipGetLastError();
   }
-  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, T, ws, s);
-  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, T, ws, s);
-  return many<MOE_Q_INT3>(A, T, ws, s);
+  if (A.q == MOE_Q_TERNARY) return many<MOE_Q_TERNARY>(A, p, T, ws, s);
+  if (A.q == MOE_Q_INT2) return many<MOE_Q_INT2>(A, p, T, ws, s);
+  return many<MOE_Q_INT3>(A, p, T, ws, s);
 }
 
 }  // namespace bqmoe

@@ -128,7 +128,7 @@ struct LinArgs {
   int64_t ldx, ldm, ldr, ldo;  // row strides in values
   int32_t K, N, q, act;
 };
-constexpr int kLinFewRows = 16;  // rows up to which the bandwidth kernel runs
+constexpr int kLinFewRows = 64;  // most rows of the bandwidth kernel
 size_t lin_ws_bytes(int K, int N, int T);
 int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream);
 // Whether the decode kernels take this layer for T tokens (LDS and register
