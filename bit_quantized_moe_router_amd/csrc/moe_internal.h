@@ -99,6 +99,7 @@ struct ScoreArgs {
   uint32_t group_magic;  // (e * group_magic) >> 20 == e / group_size for e < 1024
   int32_t team_log2;     // log2 of the lanes that look at one group
   int32_t bits;          // bits of an expert id
+  int32_t stage;         // 8-byte words of LDS a wave uses: max(E, 64)
 };
 struct ScoreOut {
   int32_t* ids;

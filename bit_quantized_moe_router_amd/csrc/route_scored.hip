@@ -11,7 +11,16 @@
 // different logits then keep their order unless they agree to about 1e-16,
 // which a 32-bit score (steps of 6e-8 below 1) would not give.  The vector
 // units run 64-bit multiply-adds at the rate of unpacked 32-bit ones, so this
-// costs little (an exponential per expert).
+// costs little (an exponential per expert).  Most rows do not need it for every
+// expert: 32-bit values with a bound on their error leave a few candidates,
+// which are ordered by their 64-bit values; a row that the bound does not
+// settle is done in 64 bits as a whole.
+//
+// What sets the time is the length of a token's chain of dependent steps, not
+// its arithmetic (one wave takes a token; its steps were stamped with the
+// clock).  Taking the k largest one after the other, each by a maximum over
+// the wave, took 770 cycles a round, 6900 of 19200 for one token at 256
+// experts, top-8.  Here all candidates are ranked at once.
 #include <hip/hip_runtime.h>
 
 #include "device_common.h"
@@ -30,10 +39,39 @@ __device__ __forceinline__ uint64_t order_key64(double v) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)(((uint64_t)dpp_u32<CTRL>((uint32_t)(u >> 32)) << 32) |
+                                          dpp_u32<CTRL>((uint32_t)u)));
+}
+// Sum over the 64 lanes, the same in every lane (the pairing of wave_sum_lanes).
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x141>(v);
+  v += dpp_f64<0x140>(v);
+  uint64_t u = (uint64_t)__double_as_longlong(v);
+  auto h = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  auto l = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+  v = __longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])) +
+      __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1]));
+  u = (uint64_t)__double_as_longlong(v);
+  h = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+  l = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+  return __longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])) +
+         __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1]));
+}
+// Maximum of a float over the lanes (no NaN among them).
+__device__ __forceinline__ float wave_max_lanes(float v) {
+  return key_value(wave_allmax_u32(order_key(v)));
+}
+__device__ __forceinline__ double readlane_f64(double v, int lane) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double(
+      (long long)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane)
+                   << 32) |
+                  (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane)));
 }
 
 // The score of a logit: m and inv_sum are the row's maximum and 1 / sum of the
@@ -57,19 +95,247 @@ __device__ __forceinline__ double key_value64(uint64_t key) {
   return __longlong_as_double((long long)((key >> 63) ? (key & 0x7FFFFFFFFFFFFFFFull) : ~key));
 }
 
-// One token by one wave (lane l holds experts l + 64 i): ids and weights of
-// the k selected experts in lanes 0..k-1.  `stage` is E keys of LDS of the
-// wave's own (read only where the choice is limited to groups).
+// Largest and second largest over the teams of 1 << log2 lanes, in all of their
+// lanes (every step pairs lanes that already agree within their halves).
+template <int CTRL>
+__device__ __forceinline__ void top2_dpp(float& a1, float& a2) {
+  const float b1 = __uint_as_float(dpp_u32<CTRL>(__float_as_uint(a1)));
+  const float b2 = __uint_as_float(dpp_u32<CTRL>(__float_as_uint(a2)));
+  a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+  a1 = fmaxf(a1, b1);
+}
+__device__ __forceinline__ void team_top2(float& a1, float& a2, int log2) {
+  if (log2 >= 1) top2_dpp<0xB1>(a1, a2);
+  if (log2 >= 2) top2_dpp<0x4E>(a1, a2);
+  if (log2 >= 3) top2_dpp<0x141>(a1, a2);
+  if (log2 >= 4) top2_dpp<0x140>(a1, a2);
+  for (int o = 16; o < (1 << log2); o <<= 1) {
+    const float b1 = __shfl_xor(a1, o, 64), b2 = __shfl_xor(a2, o, 64);
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+  }
+}
+
+// The choice by 32-bit values and their error bound (lane l holds experts
+// l + 64 i, lg their logits, bs their biases).  False where the bound does not
+// settle it: the caller then takes the whole row in 64 bits.  On true, a lane
+// with rank < k holds one selected expert: its place in the order, its id and
+// its score (up to the softmax's sum where the weights are renormalised).
+//
+// Every lane's largest value is its head.  At least m of the values are no
+// smaller than the m-th largest head, so the values from there on, compacted
+// into one lane each, hold the k largest (m = k, or k + 1 where values have an
+// error).  There are k to 4 k of them as a rule; more than 64 are left to the
+// 64-bit path.
+//
+// Errors: the hardware's exponential and reciprocal are good to one unit in
+// the last place (2^-23 relative).  Sigmoid, s <= 1: the exponential's argument
+// is off by |l| 2^-24, which s (1 - s) |l| <= 0.23 makes 0.12 * 2^-23, its
+// result's unit 0.25 * 2^-23, the sum's rounding and the reciprocal's unit
+// 1.5 * 2^-23: less than 2^-22.  Softmax of largest score q: p |ln p/q| <= 0.37 q,
+// so 0.6 * 2^-23 q, one unit of the exponential, the sum's (64-bit) and the
+// product's: less than q 2^-20.  Adding the bias rounds by 2^-24 of the sum.
+// Softmax without a bias is ranked by the logits themselves, which has no
+// error; its group values are then sums of exponentials with q = 1.
 template <int PER>
-__device__ void wave_scored_topk(const ScoreArgs& S, const float* __restrict__ L, int lane,
-                                 uint64_t* stage, int& my_id, float& my_w) {
+__device__ bool choose_32(const ScoreArgs& S, const float (&lg)[PER], const float (&bs)[PER],
+                          int lane, float* lds, int& rank, int& my_id, double& my_s) {
   const int E = S.E, k = S.k;
-  float lg[PER];
+  const bool grouped = S.topk_groups < S.n_groups, by_logit = !S.sigmoid && !S.bias;
+  // a NaN or an infinite value takes the 64-bit path
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) odd |= !(lg[i] < INFINITY);
+  float mx = 0.f, fast_sum = 1.f;
+  double inv_sum = 1.0;
+  if (!S.sigmoid) {
+    mx = lg[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mx = fmaxf(mx, lg[i]);
+    mx = wave_max_lanes(mx);
+    if (mx == -INFINITY) return false;
+    if (S.bias || !S.renorm) {
+      double s = 0.0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane + 64 * i < E) s += exp((double)lg[i] - (double)mx);
+      inv_sum = 1.0 / wave_sum64(s);
+      fast_sum = (float)inv_sum;
+    }
+  }
+  // the choice values; unit: their error's bound
+  float c[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (S.sigmoid)
+      c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * lg[i]));
+    else if (by_logit && !grouped)
+      c[i] = lg[i];
+    else
+      c[i] = __builtin_amdgcn_exp2f(1.4426950408889634f * (lg[i] - mx)) * (S.bias ? fast_sum : 1.f);
+    if (S.bias) c[i] += bs[i];
+    if (lg[i] == -INFINITY) c[i] = -INFINITY;
+    odd |= !(c[i] < INFINITY);
+  }
+  if (__ballot(odd)) return false;
+  const float unit = S.sigmoid ? 0x1p-22f : (S.bias ? fast_sum : 1.f) * 0x1p-20f;
+  uint64_t kept = ~0ull;
+  if (grouped) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (lane + 64 * i < E) lds[lane + 64 * i] = c[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int ts = 1 << S.team_log2, g = lane >> S.team_log2, gs = S.group_size;
+    float a1 = -INFINITY, a2 = -INFINITY;
+    if (g < S.n_groups)
+#pragma unroll 4
+      for (int i = lane & (ts - 1); i < gs; i += ts) {
+        const float v = lds[g * gs + i];
+        a2 = fmaxf(a2, fminf(a1, v));
+        a1 = fmaxf(a1, v);
+      }
+    team_top2(a1, a2, S.team_log2);
+    const float gv = S.group_top == 1 ? a1 : a1 + a2;
+    int better = 0;
+    for (int h = 0; h < S.n_groups; ++h) {
+      const float o =
+          __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gv), h << S.team_log2));
+      better += (o > gv || (o == gv && h < g)) ? 1 : 0;
+    }
+    const bool in = g < S.n_groups && better < S.topk_groups;
+    kept = __ballot(in);
+    // the worst group in and the best one out have to lie clearly apart
+    const float lo = -wave_max_lanes(in ? -gv : -INFINITY);
+    const float hi = wave_max_lanes(!in && g < S.n_groups ? gv : -INFINITY);
+    if (!(lo - hi > 4.f * unit + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)))) return false;
+    __builtin_amdgcn_wave_barrier();  // (the values are read; the area is used again)
+  }
+  uint32_t key[PER], head = 0u;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    lg[i] = e < E ? L[e] : -INFINITY;
+    const int ge = (int)(((uint32_t)e * S.group_magic) >> 20);  // e / group_size
+    const bool out = e >= E || (grouped && !((kept >> (ge << S.team_log2)) & 1));
+    key[i] = out ? 0u : order_key(by_logit ? lg[i] : c[i]);
+    head = max(head, key[i]);
   }
+  // t: the m-th largest head (1 where there are not m)
+  const int m = by_logit ? k : k + 1;
+  int above = 0;  // heads above this lane's
+#pragma unroll
+  for (int j = 0; j < 64; ++j)
+    above += (uint32_t)__builtin_amdgcn_readlane((int)head, j) > head ? 1 : 0;
+  uint32_t t = ~wave_allmax_u32(head && above < m ? ~head : 0u);
+  if (__popcll(__ballot(head != 0u)) < m) t = 1u;
+  // the candidates, compacted: id and logit
+  int* const cid = reinterpret_cast<int*>(lds);
+  float* const cl = lds + 64;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint64_t at = __ballot(key[i] >= t);
+    const int pos = n + __popcll(at & (lane ? (~0ull >> (64 - lane)) : 0ull));
+    if (key[i] >= t && pos < 64) {
+      cid[pos] = lane + 64 * i;
+      cl[pos] = lg[i];
+    }
+    n += __popcll(at);
+  }
+  if (n > 64) return false;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const bool cand = lane < n;
+  my_id = cid[cand ? lane : 0];
+  const float l = cl[cand ? lane : 0];
+  my_s = score_of(S, l, (double)mx, inv_sum);
+  rank = 0;
+  int same = 0;
+  if (by_logit) {
+    const uint32_t mine = order_key(l);
+    for (int j = 0; j < n; ++j) {
+      const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)mine, j);
+      rank += o > mine ? 1 : 0;
+      same += o == mine ? 1 : 0;
+    }
+  } else {
+    const double d = l == -INFINITY ? -INFINITY : my_s + (S.bias ? (double)S.bias[my_id] : 0.0);
+    for (int j = 0; j < n; ++j) {
+      const double o = readlane_f64(d, j);
+      rank += o > d ? 1 : 0;
+      same += o == d ? 1 : 0;
+    }
+    // whatever is no candidate is below t by its 32-bit value: the last one
+    // chosen has to lie above that by more than the error
+    const double edge = t == 1u ? -INFINITY
+                                : (double)key_value(t) + (double)unit +
+                                      0x1p-23 * fabs((double)key_value(t));
+    if (__ballot(cand && rank < k && !(d > edge)) && t != 1u) return false;
+  }
+  if (__ballot(cand && same > 1)) {  // equal values: the lower index first
+    const float v = by_logit ? l : 0.f;
+    const double d =
+        by_logit ? 0.0
+                 : l == -INFINITY ? -INFINITY : my_s + (S.bias ? (double)S.bias[my_id] : 0.0);
+    for (int j = 0; j < n; ++j) {
+      const int oi = __builtin_amdgcn_readlane(my_id, j);
+      const bool eq = by_logit ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)) == v
+                               : readlane_f64(d, j) == d;
+      rank += eq && oi < my_id ? 1 : 0;
+    }
+  }
+  if (!cand) rank = 64;
+  // 64-bit scores that run out at 0 are ties, which logits are not
+  if (by_logit) return !__ballot(rank < k && !(l - mx > -700.f));
+  return true;
+}
+
+template <int PER>
+__device__ void choose_64(const ScoreArgs& S, const float (&lg)[PER],
+                          const float* __restrict__ L, int lane, uint64_t* stage, int& my_id,
+                          double& my_s);
+
+// One token by one wave: a lane with rank < k returns one selected expert, its
+// place in the order and its weight.  `stage` is max(E, 64) * 8 bytes of LDS of
+// the wave's own.
+template <int PER>
+__device__ __forceinline__ void wave_scored_topk(const ScoreArgs& S, const float* __restrict__ L,
+                                                 int lane, uint64_t* stage, int& rank, int& my_id,
+                                                 float& my_w) {
+  float lg[PER], bs[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane + 64 * i;
+    lg[i] = e < S.E ? L[e] : -INFINITY;
+  }
+  if (S.bias) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bs[i] = S.bias[min(lane + 64 * i, S.E - 1)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) bs[i] = 0.f;
+  }
+  double s;
+  __builtin_amdgcn_wave_barrier();  // the last token's staging is read
+  if (!choose_32<PER>(S, lg, bs, lane, reinterpret_cast<float*>(stage), rank, my_id, s)) {
+    choose_64<PER>(S, lg, L, lane, stage, my_id, s);
+    rank = lane;
+  }
+  if (rank >= S.k) s = 0.0;
+  // weights from the scores, without the bias
+  if (S.renorm) {
+    const double den = wave_sum64(s);
+    s = den == 0.0 ? 0.0 : s / den;
+  }
+  my_w = (float)(s * (double)S.scale);
+}
+
+// The whole choice in 64 bits.
+template <int PER>
+__device__ void choose_64(const ScoreArgs& S, const float (&lg)[PER],
+                          const float* __restrict__ L, int lane, uint64_t* stage, int& my_id,
+                          double& my_s) {
+  const int E = S.E, k = S.k;
   double m = 0.0, inv_sum = 0.0;
   if (!S.sigmoid) {
     float mx = lg[0];
@@ -163,13 +429,7 @@ __device__ void wave_scored_topk(const ScoreArgs& S, const float* __restrict__ L
     key[PER - 1] = pop ? 0ull : key[PER - 1];
     my_id = lane == j ? (int)win : my_id;
   }
-  // weights from the scores, without the bias
-  double s = lane < k ? score_of(S, L[my_id], m, inv_sum) : 0.0;
-  if (S.renorm) {
-    const double den = wave_sum64(s);
-    s = den == 0.0 ? 0.0 : s / den;
-  }
-  my_w = (float)(s * (double)S.scale);
+  my_s = score_of(S, L[my_id], m, inv_sum);
 }
 
 // Lanes whose `key` (< 2^bits) equals this lane's, among `active` lanes.
@@ -231,6 +491,26 @@ __device__ __forceinline__ void write_tiles(const ScoreOut& O, int T, int k, int
   if (threadIdx.x == 0) O.ctrl[0] = ntiles + nsh;
 }
 
+// The decode slot list's header, the shared expert's slot and the empty ones,
+// by threads i of n (n >= T).
+__device__ __forceinline__ void write_other_slots(const ScoreOut& O, int T, int rows,
+                                                  int n_active, int i, int n) {
+  const int n_slots = n_active + (O.n_shared ? 1 : 0);
+  if (i == 0) O.slots[0] = n_slots;
+  if (O.n_shared && i < T) {
+    int32_t* rec = O.slots + kSlotRec * (1 + n_active);
+    if (i == 0) {
+      rec[0] = -1;
+      rec[1] = rows;
+      rec[2] = T;
+      rec[3] = 0;
+    }
+    rec[kSlotTok + i] = i;
+  }
+  for (int s = n_slots + i; s < O.max_slots; s += n)
+    for (int j = 0; j < kSlotTok; ++j) O.slots[kSlotRec * (1 + s) + j] = 0;
+}
+
 // ------------------------------------------------------------ few tokens
 // One block does everything for at most 1024 rows: the waves take the tokens
 // in turn, then the rows sit 64 to a wave, each wave ranks its rows among
@@ -245,18 +525,65 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
   __shared__ int s_tot[THREADS / 64];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int E = S.E, k = S.k, rows = T * k;
-  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * E;
+  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * S.stage;
   for (int t = wave; t < T; t += THREADS / 64) {
-    int id;
+    int j, id;
     float w;
-    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, id, w);
-    if (lane < k) {
-      O.ids[t * k + lane] = id;
-      O.w[t * k + lane] = w;
-      s_row[t * k + lane] = id;
+    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, j, id, w);
+    if (j < k) {
+      O.ids[t * k + j] = id;
+      O.w[t * k + j] = w;
+      s_row[t * k + j] = id;
     }
   }
   __syncthreads();
+  if (rows <= 64 && !O.tiles) {
+    // at most 64 rows, one per lane of wave 0: each row's place from ballots
+    // over the bits of the expert ids; thread e counts the rows of expert e and
+    // of those before it
+    if (wave == 0) {
+      const bool act = lane < rows;
+      const int id = act ? s_row[lane] : 0;
+      uint64_t eq = __ballot(act), less = 0;
+      for (int b = S.bits - 1; b >= 0; --b) {
+        const bool bit = (id >> b) & 1;
+        const uint64_t m1 = __ballot(act && bit);
+        less |= bit ? eq & ~m1 : 0ull;
+        eq &= bit ? m1 : ~m1;
+      }
+      const uint64_t below = lane ? (~0ull >> (64 - lane)) : 0ull;
+      const int rk = __popcll(eq & below), off = __popcll(less);
+      const uint64_t first = __ballot(act && rk == 0);
+      const int slot = __popcll(less & first), n_active = __popcll(first);
+      if (act) {
+        O.perm_tok[off + rk] = lane / k;
+        O.inv_row[lane] = off + rk;
+        if (O.slots) {
+          int32_t* rec = O.slots + kSlotRec * (1 + slot);
+          rec[kSlotTok + rk] = lane / k;
+          if (rk == 0) {
+            rec[0] = id;
+            rec[1] = off;
+            rec[2] = __popcll(eq);
+            rec[3] = O.alt_select && O.alt_select[id] ? 1 : 0;
+          }
+        }
+      }
+      if (O.slots) write_other_slots(O, T, rows, n_active, lane, 64);
+    }
+    for (int e = tid; e < E; e += THREADS) {
+      int cnt = 0, off = 0;
+      for (int r = 0; r < rows; ++r) {
+        const int o = s_row[r];
+        cnt += o == e ? 1 : 0;
+        off += o < e ? 1 : 0;
+      }
+      O.counts[e] = cnt;
+      O.offsets[e] = off;
+    }
+    if (tid == 0) O.offsets[E] = rows;
+    return;
+  }
   const int chunks = (rows + 63) >> 6;
   int* cnt = reinterpret_cast<int*>(sm);
   for (int i = tid; i < chunks * E; i += THREADS) cnt[i] = 0;
@@ -317,22 +644,7 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
       O.inv_row[r] = pos;
     }
   }
-  if (O.slots) {
-    const int n_slots = n_active + (O.n_shared ? 1 : 0);
-    if (tid == 0) O.slots[0] = n_slots;
-    if (O.n_shared && tid < T) {
-      int32_t* rec = O.slots + kSlotRec * (1 + n_active);
-      if (tid == 0) {
-        rec[0] = -1;
-        rec[1] = rows;
-        rec[2] = T;
-        rec[3] = 0;
-      }
-      rec[kSlotTok + tid] = tid;
-    }
-    for (int s = n_slots + tid; s < O.max_slots; s += THREADS)
-      for (int j = 0; j < kSlotTok; ++j) O.slots[kSlotRec * (1 + s) + j] = 0;
-  }
+  if (O.slots) write_other_slots(O, T, rows, n_active, tid, THREADS);
   if (O.tiles) write_tiles(O, T, k, E, tid < E ? total : 0, off, s_tot);
 }
 
@@ -353,16 +665,16 @@ __global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int E = S.E, k = S.k;
   const int t0 = blockIdx.x * tb, t1 = min(T, t0 + tb);
-  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * E;
-  int* s_row = reinterpret_cast<int*>(sm + (size_t)NW * E * 8);
+  uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * S.stage;
+  int* s_row = reinterpret_cast<int*>(sm + (size_t)NW * S.stage * 8);
   for (int t = t0 + wave; t < t1; t += NW) {
-    int id;
+    int j, id;
     float wt;
-    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, id, wt);
-    if (lane < k) {
-      ids[(size_t)t * k + lane] = id;
-      w[(size_t)t * k + lane] = wt;
-      s_row[(t - t0) * k + lane] = id;
+    wave_scored_topk<PER>(S, logits + (size_t)t * E, lane, stage, j, id, wt);
+    if (j < k) {
+      ids[(size_t)t * k + j] = id;
+      w[(size_t)t * k + j] = wt;
+      s_row[(t - t0) * k + j] = id;
     }
   }
   __syncthreads();
@@ -422,7 +734,7 @@ __global__ __launch_bounds__(1024) void k_scored_place(const int32_t* __restrict
   const int parts = max(1, 1024 / E), part = tid / E, e = tid - part * E;
   if (part < parts) {
     int all = 0, base = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int b = part; b < nblk; b += parts) {
       const int v = hist[(size_t)b * E + e];
       all += v;
@@ -497,7 +809,7 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   S.group_magic = ((1u << 20) + S.group_size - 1) / S.group_size;
   S.team_log2 = 6 - (C->n_groups > 1 ? bits_for(C->n_groups) : 0);
   S.bits = bits_for(E);
-  const bool grouped = S.topk_groups < S.n_groups;
+  S.stage = E > 64 ? E : 64;
   ScoreOut O = out;
   O.ids = R->topk_ids;
   O.w = R->topk_w;
@@ -509,7 +821,7 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   if (T <= kScoredFewTokens && rows <= kScoredFewRows) {
     const int threads = E <= 256 && T <= 4 && rows <= 256 ? 256 : 1024;
     const size_t cnt = (size_t)((rows + 63) / 64) * E * 4;
-    const size_t stg = grouped ? (size_t)(threads / 64) * E * 8 : 0;
+    const size_t stg = (size_t)(threads / 64) * S.stage * 8;
     const size_t lds = cnt > stg ? cnt : stg;
 #define BQ_FEW(PER, TH)                                                                       \
   do {                                                                                        \
@@ -544,7 +856,7 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   const int nblk = (T + tb - 1) / tb;
   int32_t* hist = (int32_t*)scratch;
   int32_t* lrank = hist + (size_t)nblk * E;
-  const size_t lds = (size_t)waves * E * 8 + (size_t)tb * k * 4;
+  const size_t lds = (size_t)waves * S.stage * 8 + (size_t)tb * k * 4;
 #define BQ_SEL(PER, TH)                                                                        \
   do {                                                                                         \
     const void* f = (const void*)k_scored_select<PER, TH>;                                     \
@@ -566,7 +878,7 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   else
     BQ_SEL(16, 512);
 #undef BQ_SEL
-  const int sb = (nblk + 63) / 64;
+  const int sb = (nblk + 255) / 256;
   hipLaunchKernelGGL(k_scored_place, dim3((nblk + sb - 1) / sb), dim3(1024), 0, s, R->topk_ids, T,
                      E, k, tb, sb, nblk, hist, lrank, O);
   return (int)hipGetLastError();
