@@ -122,11 +122,12 @@ __device__ __forceinline__ void team_top2(float& a1, float& a2, int log2) {
 // with rank < k holds one selected expert: its place in the order, its id and
 // its score (up to the softmax's sum where the weights are renormalised).
 //
-// Every lane's largest value is its head.  At least m of the values are no
-// smaller than the m-th largest head, so the values from there on, compacted
-// into one lane each, hold the k largest (m = k, or k + 1 where values have an
-// error).  There are k to 4 k of them as a rule; more than 64 are left to the
-// 64-bit path.
+// Every lane's largest value is its head.  Where m heads are at least t, so are
+// m values, and all values from t on, compacted into one lane each, hold the k
+// largest (m = k, or k + 1 where values have an error).  t is found by
+// bisection over the heads' range, with a ballot a step, until m to m + 4 heads
+// are left.  There are k to 4 k candidates as a rule; more than 64 are left to
+// the 64-bit path.
 //
 // Errors: the hardware's exponential and reciprocal are good to one unit in
 // the last place (2^-23 relative).  Sigmoid, s <= 1: the exponential's argument
@@ -206,8 +207,12 @@ __device__ bool choose_32(const ScoreArgs& S, const float (&lg)[PER], const floa
     const bool in = g < S.n_groups && better < S.topk_groups;
     kept = __ballot(in);
     // the worst group in and the best one out have to lie clearly apart
-    const float lo = -wave_max_lanes(in ? -gv : -INFINITY);
-    const float hi = wave_max_lanes(!in && g < S.n_groups ? gv : -INFINITY);
+    const uint64_t at_lo = __ballot(g < S.n_groups && better == S.topk_groups - 1);
+    const uint64_t at_hi = __ballot(g < S.n_groups && better == S.topk_groups);
+    const float lo = __int_as_float(__builtin_amdgcn_readlane(
+        __float_as_int(gv), (int)__ffsll((unsigned long long)at_lo) - 1));
+    const float hi = __int_as_float(__builtin_amdgcn_readlane(
+        __float_as_int(gv), (int)__ffsll((unsigned long long)at_hi) - 1));
     if (!(lo - hi > 4.f * unit + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)))) return false;
     __builtin_amdgcn_wave_barrier();  // (the values are read; the area is used again)
   }
@@ -220,14 +225,21 @@ __device__ bool choose_32(const ScoreArgs& S, const float (&lg)[PER], const floa
     key[i] = out ? 0u : order_key(by_logit ? lg[i] : c[i]);
     head = max(head, key[i]);
   }
-  // t: the m-th largest head (1 where there are not m)
   const int m = by_logit ? k : k + 1;
-  int above = 0;  // heads above this lane's
-#pragma unroll
-  for (int j = 0; j < 64; ++j)
-    above += (uint32_t)__builtin_amdgcn_readlane((int)head, j) > head ? 1 : 0;
-  uint32_t t = ~wave_allmax_u32(head && above < m ? ~head : 0u);
-  if (__popcll(__ballot(head != 0u)) < m) t = 1u;
+  uint32_t t = ~wave_allmax_u32(head ? ~head : 0u);  // the smallest head
+  if (__popcll(__ballot(head != 0u)) < m)
+    t = 1u;  // fewer heads than m: every value is a candidate
+  else
+    for (uint32_t hi = wave_allmax_u32(head) + 1u; hi - t > 1u;) {
+      const uint32_t mid = t + ((hi - t) >> 1);
+      const int cnt = __popcll(__ballot(head >= mid));
+      if (cnt >= m)
+        t = mid;
+      else
+        hi = mid;
+      if (cnt >= m && cnt <= m + 4) break;
+    }
+  t = (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
   // the candidates, compacted: id and logit
   int* const cid = reinterpret_cast<int*>(lds);
   float* const cl = lds + 64;
@@ -521,10 +533,11 @@ template <int PER, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float* __restrict__ logits,
                                                         int T, ScoreOut O) {
   extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
-  __shared__ int s_row[kScoredFewRows];
+  __shared__ __attribute__((aligned(16))) int s_row[kScoredFewRows];
   __shared__ int s_tot[THREADS / 64];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int E = S.E, k = S.k, rows = T * k;
+  if (tid < ((4 - rows) & 3)) s_row[rows + tid] = 0x7FFFFFFF;
   uint64_t* stage = reinterpret_cast<uint64_t*>(sm) + (size_t)wave * S.stage;
   for (int t = wave; t < T; t += THREADS / 64) {
     int j, id;
@@ -573,10 +586,11 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
     }
     for (int e = tid; e < E; e += THREADS) {
       int cnt = 0, off = 0;
-      for (int r = 0; r < rows; ++r) {
-        const int o = s_row[r];
-        cnt += o == e ? 1 : 0;
-        off += o < e ? 1 : 0;
+#pragma unroll 4
+      for (int r = 0; r < rows; r += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(s_row + r);  // (padded with no expert)
+        cnt += (o.x == e ? 1 : 0) + (o.y == e ? 1 : 0) + (o.z == e ? 1 : 0) + (o.w == e ? 1 : 0);
+        off += (o.x < e ? 1 : 0) + (o.y < e ? 1 : 0) + (o.z < e ? 1 : 0) + (o.w < e ? 1 : 0);
       }
       O.counts[e] = cnt;
       O.offsets[e] = off;
@@ -658,7 +672,7 @@ __global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
                                                            const float* __restrict__ logits, int T,
                                                            int tb, int32_t* __restrict__ ids,
                                                            float* __restrict__ w,
-                                                           int32_t* __restrict__ hist,
+                                                           uint16_t* __restrict__ hist,
                                                            int32_t* __restrict__ lrank) {
   extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
   constexpr int NW = THREADS / 64;
@@ -698,14 +712,16 @@ __global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
     if (act && (peers & lt) == 0) cnt[wave * E + e] = base + __popcll(peers);
   }
   __syncthreads();
-  for (int e = tid; e < E; e += THREADS) {
+  const int Ep = (E + 7) & ~7;
+  for (int e = tid; e < Ep; e += THREADS) {
     int run = 0;
-    for (int v = 0; v < NW; ++v) {
-      const int c = cnt[v * E + e];
-      cnt[v * E + e] = run;
-      run += c;
-    }
-    hist[(size_t)blockIdx.x * E + e] = run;
+    if (e < E)
+      for (int v = 0; v < NW; ++v) {
+        const int c = cnt[v * E + e];
+        cnt[v * E + e] = run;
+        run += c;
+      }
+    hist[(size_t)blockIdx.x * Ep + e] = (uint16_t)run;  // at most 8192 rows a block
   }
   __syncthreads();
   for (int c = c0; c < c1; ++c) {
@@ -716,11 +732,12 @@ __global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
 
 // Block b places the rows of the select blocks [b * sb, (b + 1) * sb).  Each
 // block sums the histogram's columns itself (all of it for the offsets, the
-// blocks before its own for its first base): nblk * E integers from L2, less
-// than a launch in between would cost.
+// blocks before its own for its first base), eight 16-bit counts a load: 128 KB
+// from L2 at 256 experts and blocks, less than a launch in between would cost
+// (4.8 us of this kernel's 7.6 with 32-bit counts one by one).
 __global__ __launch_bounds__(1024) void k_scored_place(const int32_t* __restrict__ ids, int T, int E,
                                                        int k, int tb, int sb, int nblk,
-                                                       const int32_t* __restrict__ hist,
+                                                       const uint16_t* __restrict__ hist,
                                                        const int32_t* __restrict__ lrank,
                                                        ScoreOut O) {
   __shared__ int s_all[MOE_MAX_EXPERTS], s_base[MOE_MAX_EXPERTS];
@@ -730,18 +747,28 @@ __global__ __launch_bounds__(1024) void k_scored_place(const int32_t* __restrict
   s_all[tid] = 0;
   s_base[tid] = 0;
   __syncthreads();
-  // thread = (expert, one of `parts` interleaved sets of select blocks); integer sums only
-  const int parts = max(1, 1024 / E), part = tid / E, e = tid - part * E;
+  // thread = (eight experts, one of `parts` interleaved sets of select blocks); integer sums only
+  const int V = (E + 7) / 8, parts = min(1024 / V, 128), part = tid / V, v = tid - part * V;
   if (part < parts) {
-    int all = 0, base = 0;
-#pragma unroll 16
+    int all[8], base[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) all[j] = base[j] = 0;
+#pragma unroll 8
     for (int b = part; b < nblk; b += parts) {
-      const int v = hist[(size_t)b * E + e];
-      all += v;
-      base += b < b0 ? v : 0;
+      const u32x4 h = *reinterpret_cast<const u32x4*>(hist + ((size_t)b * V + v) * 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = (int)((h[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+        all[j] += c;
+        base[j] += b < b0 ? c : 0;
+      }
     }
-    atomicAdd(&s_all[e], all);
-    atomicAdd(&s_base[e], base);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * v + j < E) {
+        atomicAdd(&s_all[8 * v + j], all[j]);
+        atomicAdd(&s_base[8 * v + j], base[j]);
+      }
   }
   __syncthreads();
   const int total = tid < E ? s_all[tid] : 0;
@@ -764,8 +791,9 @@ __global__ __launch_bounds__(1024) void k_scored_place(const int32_t* __restrict
       O.perm_tok[pos] = r / k;
       O.inv_row[r] = pos;
     }
+    if (b + 1 == b1) break;
     __syncthreads();
-    if (tid < E) s_base[tid] += hist[(size_t)b * E + tid];
+    if (tid < E) s_base[tid] += hist[(size_t)b * V * 8 + tid];
   }
 }
 
@@ -788,7 +816,8 @@ static int scored_waves(int E) { return E <= 256 ? 16 : 8; }
 size_t scored_ws_bytes(const moe_layer* L, int T) {
   const int tb = scored_block_tokens(T, L->top_k, scored_waves(L->n_experts));
   const size_t nblk = ((size_t)T + tb - 1) / tb;
-  return 4 * (nblk * (size_t)L->n_experts + (size_t)T * L->top_k) + 256;
+  const size_t hist = 2 * nblk * (((size_t)L->n_experts + 7) & ~size_t(7));
+  return ((hist + 255) & ~size_t(255)) + 4 * (size_t)T * L->top_k;
 }
 
 int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_routing* R,
@@ -854,8 +883,9 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   }
   const int waves = scored_waves(E), tb = scored_block_tokens(T, k, waves);
   const int nblk = (T + tb - 1) / tb;
-  int32_t* hist = (int32_t*)scratch;
-  int32_t* lrank = hist + (size_t)nblk * E;
+  uint16_t* hist = (uint16_t*)scratch;
+  int32_t* lrank =
+      (int32_t*)(scratch + ((2 * (size_t)nblk * ((E + 7) & ~7) + 255) & ~size_t(255)));
   const size_t lds = (size_t)waves * S.stage * 8 + (size_t)tb * k * 4;
 #define BQ_SEL(PER, TH)                                                                        \
   do {                                                                                         \
