@@ -333,14 +333,23 @@ def make_scoring(score: int, n_groups: int = 1, topk_groups: int = 1, group_top:
     """A router by scores (MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID); choice_bias: device fp32 [E]
     added to the scores for the choice only."""
     if isinstance(choice_bias, torch.Tensor) and (choice_bias.dtype != torch.float32
-                                                  or not choice_bias.is_contiguous()):
-        raise MoeError(MOE_ERR_INVALID_ARG, "make_scoring: choice_bias must be contiguous float32")
+                                                  or not choice_bias.is_contiguous()
+                                                  or not choice_bias.is_cuda):
+        raise MoeError(MOE_ERR_INVALID_ARG,
+                       "make_scoring: choice_bias must be contiguous float32 on the GPU")
     return Scoring(moe_scoring(score, n_groups, topk_groups, group_top, int(renorm), scale,
                                _ptr(choice_bias)), choice_bias)
 
 
+def _check_bias(layer: Layer, scoring: Scoring, what: str):
+    b = scoring.choice_bias
+    if isinstance(b, torch.Tensor) and b.numel() != layer.c.n_experts:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: choice_bias must hold one value per expert")
+
+
 def moe_route_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int, routing: Routing, ws,
                      stream=None):
+    _check_bias(layer, scoring, "moe_route_scored")
     st = load().moe_route_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x), T, flags,
                                  ctypes.byref(routing.c), _ptr(ws),
                                  0 if ws is None else ws.numel(), _stream(stream))
@@ -349,6 +358,7 @@ def moe_route_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int, rout
 
 def moe_forward_decode_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int,
                               routing: Routing, ws, out, stream=None):
+    _check_bias(layer, scoring, "moe_forward_decode_scored")
     st = load().moe_forward_decode_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x),
                                           T, flags, ctypes.byref(routing.c), _ptr(ws),
                                           0 if ws is None else ws.numel(), _ptr(out),
@@ -358,6 +368,7 @@ def moe_forward_decode_scored(layer: Layer, scoring: Scoring, x, T: int, flags: 
 
 def moe_forward_prefill_scored(layer: Layer, scoring: Scoring, x, T: int, flags: int,
                                routing: Routing, ws, out, stream=None):
+    _check_bias(layer, scoring, "moe_forward_prefill_scored")
     st = load().moe_forward_prefill_scored(ctypes.byref(layer.c), ctypes.byref(scoring.c), _ptr(x),
                                            T, flags, ctypes.byref(routing.c), _ptr(ws),
                                            0 if ws is None else ws.numel(), _ptr(out),
@@ -372,8 +383,8 @@ class Linear:
     def __init__(self, c: moe_linear, tensors: tuple = ()):
         self.c, self.tensors, self.ref = c, tensors, ctypes.byref(c)
         on = {t.get_device() for t in tensors if isinstance(t, torch.Tensor)}
-        if len(on) > 1:
-            raise MoeError(MOE_ERR_INVALID_ARG, "make_linear: w and bias are on different devices")
+        if len(on) > 1 or -1 in on:
+            raise MoeError(MOE_ERR_INVALID_ARG, "make_linear: w and bias must be on one GPU")
         self.device = on.pop() if on else -1  # -1: addresses, not tensors
 
 

@@ -396,12 +396,12 @@ extern "C" moe_status moe_linear_forward(const moe_linear* P, const uint16_t* x,
   if (residual && !(residual == out && residual_stride == out_stride) &&
       overlaps(residual, rows_bytes(T, residual_stride, P->N), out, ob))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = lin_ws_bytes(P->K, P->N, T);
-  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  if (!aligned(ws, 256) || overlaps(ws, need, out, ob)) return MOE_ERR_INVALID_ARG;
-  if (overlaps(ws, need, x, rows_bytes(T, x_stride, P->K)) ||
-      (mul && overlaps(ws, need, mul, rows_bytes(T, mul_stride, P->N))) ||
-      (residual && overlaps(ws, need, residual, rows_bytes(T, residual_stride, P->N))))
+  const size_t need = lin_ws_need(P->K, P->N, T);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && (!aligned(ws, 256) || overlaps(ws, need, out, ob) ||
+               overlaps(ws, need, x, rows_bytes(T, x_stride, P->K)) ||
+               (mul && overlaps(ws, need, mul, rows_bytes(T, mul_stride, P->N))) ||
+               (residual && overlaps(ws, need, residual, rows_bytes(T, residual_stride, P->N)))))
     return MOE_ERR_INVALID_ARG;
   const PackedLayout pl = packed_layout(P->qtype, P->K, P->N);
   const LinArgs A = {(const uint8_t*)P->w, pl.plane1, pl.scales, P->bias,  x,

@@ -79,7 +79,10 @@ __device__ __forceinline__ void finish(const LinArgs& A, float v, int t, int n) 
 
 // Four consecutive columns at once (8-byte loads and stores).
 __device__ __forceinline__ void finish4(const LinArgs& A, f32x4 v, int t, int n) {
-  if (A.bias) v += *reinterpret_cast<const f32x4*>(A.bias + n);
+  if (A.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += A.bias[n + j];
+  }
   for_act(A.act, [&](auto ac) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = activate<decltype(ac)::value>(v[j]);
@@ -973,10 +976,17 @@ static LinPlan lin_plan(int K, int N, int T) {
   return best;
 }
 
-size_t lin_ws_bytes(int K, int N, int T) {
+// What a call for T rows needs, and what any call for up to T rows may (a
+// split needs at most 512 64-row or 768 32-row tiles of 128 columns).
+size_t lin_ws_need(int K, int N, int T) {
   const LinPlan p = lin_plan(K, N, T);
-  if (p.kind != -1 || p.splits == 1) return 256;
-  return ((size_t)p.splits * T * N * 4 + 255) & ~size_t(255);
+  return p.kind == -1 && p.splits > 1 ? (size_t)p.splits * T * N * 4 : 0;
+}
+size_t lin_ws_bytes(int K, int N, int T) {
+  if (T <= 16) return 256;
+  const size_t most = (size_t)512 * 64 * 128 * 4;
+  const size_t all = (size_t)((K / 128 + kSomeKb - 1) / kSomeKb) * T * N * 4;
+  return ((all < most ? all : most) + 255) & ~size_t(255);
 }
 
 template <bool Q3>

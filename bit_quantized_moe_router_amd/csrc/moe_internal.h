@@ -130,7 +130,8 @@ struct LinArgs {
   int32_t K, N, q, act;
 };
 constexpr int kLinFewRows = 64;  // most rows of the bandwidth kernel
-size_t lin_ws_bytes(int K, int N, int T);
+size_t lin_ws_need(int K, int N, int T);   // for T rows
+size_t lin_ws_bytes(int K, int N, int T);  // for any number up to T
 int launch_linear(const LinArgs& A, int T, uint8_t* ws, void* stream);
 // Whether the decode kernels take this layer for T tokens (LDS and register
 // limits of their launch shapes).

@@ -504,9 +504,9 @@ __device__ __forceinline__ void write_tiles(const ScoreOut& O, int T, int k, int
 }
 
 // The decode slot list's header, the shared expert's slot and the empty ones,
-// by threads i of n (n >= T).
+// by lane i of a wave (T <= 8).
 __device__ __forceinline__ void write_other_slots(const ScoreOut& O, int T, int rows,
-                                                  int n_active, int i, int n) {
+                                                  int n_active, int i) {
   const int n_slots = n_active + (O.n_shared ? 1 : 0);
   if (i == 0) O.slots[0] = n_slots;
   if (O.n_shared && i < T) {
@@ -519,13 +519,14 @@ __device__ __forceinline__ void write_other_slots(const ScoreOut& O, int T, int 
     }
     rec[kSlotTok + i] = i;
   }
-  for (int s = n_slots + i; s < O.max_slots; s += n)
+  for (int s = n_slots + i; s < O.max_slots; s += 64)
     for (int j = 0; j < kSlotTok; ++j) O.slots[kSlotRec * (1 + s) + j] = 0;
 }
 
 // ------------------------------------------------------------ few tokens
 // One block does everything for at most 1024 rows: the waves take the tokens
-// in turn, then the rows sit 64 to a wave, each wave ranks its rows among
+// in turn, then (beyond 64 rows, or where the tile list is wanted; decode has
+// neither) the rows sit 64 to a wave, each wave ranks its rows among
 // themselves by ballots over the expert id's bits, and thread e sums the
 // waves' counts of expert e and scans them over the experts.  cnt is
 // [chunks][E] in LDS.
@@ -582,7 +583,7 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
           }
         }
       }
-      if (O.slots) write_other_slots(O, T, rows, n_active, lane, 64);
+      if (O.slots) write_other_slots(O, T, rows, n_active, lane);
     }
     for (int e = tid; e < E; e += THREADS) {
       int cnt = 0, off = 0;
@@ -628,24 +629,11 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
       total += v;
     }
   int all;
-  const int ex = block_scan(total | (total ? 1 << 16 : 0), s_tot, all);  // rows <= 1024 < 2^16
-  const int off = ex & 0xFFFF, slot = ex >> 16;
-  const int n_active = all >> 16;
+  const int off = block_scan(total, s_tot, all);
   if (tid < E) {
     O.counts[tid] = total;
     O.offsets[tid] = off;
     for (int c = 0; c < chunks; ++c) cnt[c * E + tid] += off;
-    if (O.slots && total) {
-      int32_t* rec = O.slots + kSlotRec * (1 + slot);
-      rec[0] = tid;
-      rec[1] = off;
-      rec[2] = total;
-      rec[3] = O.alt_select && O.alt_select[tid] ? 1 : 0;
-      // the tokens of the slot's rows, in ascending order (T <= 8 with slots)
-      int n = 0;
-      for (int r = 0; r < rows; ++r)
-        if (s_row[r] == tid) rec[kSlotTok + n++] = r / k;
-    }
   }
   if (tid == 0) O.offsets[E] = rows;
   __syncthreads();
@@ -658,7 +646,6 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
       O.inv_row[r] = pos;
     }
   }
-  if (O.slots) write_other_slots(O, T, rows, n_active, tid, THREADS);
   if (O.tiles) write_tiles(O, T, k, E, tid < E ? total : 0, off, s_tot);
 }
 

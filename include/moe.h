@@ -360,7 +360,8 @@ typedef struct {
   const float* bias; /* device fp32 [N], or NULL */
 } moe_linear;
 
-/* Device workspace of moe_linear_forward for T rows (0 if the description is invalid). */
+/* Device workspace that moe_linear_forward needs for any number of rows up to
+ * T (at most 16 MiB; 0 if the description is invalid). */
 size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T);
 
 /*   x        : device bf16 [T][K], rows x_stride values apart
@@ -369,7 +370,9 @@ size_t moe_linear_workspace_bytes(const moe_linear* P, int32_t T);
  *   out      : device bf16 [T][N], rows out_stride apart; it may be mul or
  *              residual itself (same address and stride), and overlaps nothing
  *              else.  Only the N values of its T rows are written.
- *   ws       : device workspace of ws_bytes >= moe_linear_workspace_bytes(P, T)
+ *   ws       : device workspace of ws_bytes >= moe_linear_workspace_bytes(P, T);
+ *              calls whose work may overlap need one each.  Some numbers of
+ *              rows use none of it, and NULL does for 16 or fewer.
  * Rows start at 16-byte aligned addresses: pointers are 16-byte aligned and
  * strides multiples of 8, at least the row's length, at most
  * MOE_MAX_LINEAR_STRIDE.

@@ -60,23 +60,32 @@ def test_a_null_or_senseless_description_is_refused():
 
 @pytest.mark.parametrize("T", [2, 100])
 def test_operands_are_checked_before_any_launch(T):
-    P, bad = _desc(), bq.MOE_ERR_INVALID_ARG
+    # (2048 x 48 at 100 rows: K is split, so the workspace is used)
+    P, bad = _desc(K=256 if T == 2 else 2048), bq.MOE_ERR_INVALID_ARG
     other = FAKE + (1 << 34)
-    for kw in (dict(T=-1), dict(x=None), dict(x=FAKE + 2), dict(xs=248), dict(xs=260),
+    for kw in (dict(T=-1), dict(x=None), dict(x=FAKE + 2), dict(xs=P.K - 8), dict(xs=P.K + 4),
                dict(out=None), dict(out=FAKE + 8), dict(os_=40), dict(os_=52),
                dict(mul=other + 2), dict(mul=other, ms=44), dict(res=other + 8),
-               dict(res=other, rs=50), dict(ws=FAKE + (1 << 37) + 8),
+               dict(res=other, rs=50),
                dict(out=FAKE), dict(out=FAKE + 256),              # over x
                dict(mul=FAKE + (1 << 36) + 16),                   # out shifted against mul
-               dict(res=FAKE + (1 << 36), rs=56),                 # another stride
-               dict(ws=FAKE + (1 << 36))):                        # workspace over out
+               dict(res=FAKE + (1 << 36), rs=56)):                # another stride
         kw = dict(T=T, **kw) if "T" not in kw else kw
         assert _call(P, **kw) == bad, kw
     assert _call(_desc(w=None), T=T) == bad
     assert _call(_desc(w=FAKE + 64), T=T) == bad
     assert _call(_desc(bias=FAKE + 2), T=T) == bad
-    assert _call(P, T=T, ws=None) == bq.MOE_ERR_WORKSPACE
-    assert _call(P, T=T, ws_bytes=8) == bq.MOE_ERR_WORKSPACE
+    if T == 100:
+        assert _call(P, T=T, ws=None) == bq.MOE_ERR_WORKSPACE
+        assert _call(P, T=T, ws_bytes=8) == bq.MOE_ERR_WORKSPACE
+        for ws in (FAKE + (1 << 37) + 8, FAKE, FAKE + (1 << 36)):  # unaligned, over x, over out
+            assert _call(P, T=T, ws=ws) == bad
+        assert _call(P, T=T, mul=other, ws=other) == bad
+        assert _call(P, T=T, res=other, ws=other) == bad
+    big = (1 << 23) + 8
+    assert _call(P, T=T, xs=big) == bq.MOE_ERR_UNSUPPORTED
+    assert _call(P, T=T, os_=big) == bq.MOE_ERR_UNSUPPORTED
+    assert _call(P, T=T, res=other, rs=big) == bq.MOE_ERR_UNSUPPORTED
     assert _call(P, T=(1 << 24) + 1, ws_bytes=1 << 50) == bq.MOE_ERR_UNSUPPORTED
     assert _call(P, T=0, x=None, out=None, ws=None) == bq.MOE_OK
 
@@ -93,12 +102,21 @@ def test_binding_refuses_tensors_that_do_not_fit():
         bq.make_linear(256, 48, 2, FAKE, bias=torch.zeros(47))
     with pytest.raises(bq.MoeError):
         bq.make_linear(256, 48, 2, torch.zeros(100, dtype=torch.uint8))
+    with pytest.raises(bq.MoeError):  # a host tensor
+        bq.make_linear(256, 48, 2, torch.zeros(bq.moe_packed_bytes(2, 256, 48), dtype=torch.uint8))
 
 
-def test_workspace_grows_with_the_rows():
+def test_a_workspace_for_many_rows_does_for_fewer():
     lib = bq.load()
-    s = [lib.moe_linear_workspace_bytes(ctypes.byref(_desc()), T) for T in (0, 1, 65, 1000, 9000)]
-    assert all(v > 0 for v in s) and s == sorted(s)
+    for K, N in ((256, 48), (8192, 4096), (4096, 16), (65536, 65536)):
+        P = _desc(K=K, N=N)
+        s = [lib.moe_linear_workspace_bytes(ctypes.byref(P), T) for T in (0, 1, 17, 65, 1000, 9000)]
+        assert all(0 < v <= 16 << 20 for v in s) and s == sorted(s)
+        for T in list(range(17, 400, 7)) + [1000, 3000, 9000]:
+            # a size that covers T: the call passes that check and fails at the next one
+            ws = lib.moe_linear_workspace_bytes(ctypes.byref(P), T)
+            assert _call(P, T=T, ws_bytes=ws, ws=FAKE + (1 << 50) + 8, out=FAKE) == \
+                bq.MOE_ERR_INVALID_ARG
 
 
 # ------------------------------------------------------------------------------ the GPU's
@@ -343,9 +361,10 @@ def test_in_place_on_the_residual_stream_and_deterministic(T, K, N):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 33, 150])
-def test_captured_into_a_graph(T):
-    c = Case(T, 640, 144, 2, act="gelu_tanh", bias=True)
+@pytest.mark.parametrize("T,K,N", [(1, 640, 144), (33, 640, 144), (150, 2048, 144),
+                                   (MANY[0], 256, MANY[1])])
+def test_captured_into_a_graph(T, K, N):
+    c = Case(T, K, N, 2, act="gelu_tanh", bias=True)
     lin = c.linear()
     ws = bq.alloc_linear_workspace(lin, T)
     x = torch.zeros(T, c.K, dtype=torch.bfloat16, device=DEV)
@@ -357,7 +376,7 @@ def test_captured_into_a_graph(T):
         with torch.cuda.graph(g, stream=s):
             bq.moe_linear_forward(lin, x, T, out, ws)
     for seed in range(3):
-        d = Case(T, 640, 144, 2, act="gelu_tanh", bias=True, seed=seed)
+        d = Case(T, K, N, 2, act="gelu_tanh", bias=True, seed=seed)
         x.copy_(d.x)
         g.replay()
         torch.cuda.synchronize()

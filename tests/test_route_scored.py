@@ -84,8 +84,8 @@ def test_argument_errors_are_those_of_the_other_router(fn):
         assert _call(fn, _layer(), S, T=0) == bq.MOE_OK
 
 
-def test_bias_tensor_must_be_contiguous_float32():
-    for b in (torch.zeros(4, dtype=torch.float64), torch.zeros(8)[::2]):
+def test_bias_tensor_must_be_contiguous_float32_on_the_gpu():
+    for b in (torch.zeros(4, dtype=torch.float64), torch.zeros(8)[::2], torch.zeros(8)):
         with pytest.raises(bq.MoeError):
             bq.make_scoring(SIG, choice_bias=b)
 
@@ -222,9 +222,21 @@ def test_softmax_without_groups_is_the_layers_own_router():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 8, 77, 900])
-def test_captured_into_a_graph_and_on_another_stream(T):
-    E, k = 96, 4
+def test_bias_of_another_number_of_experts_is_refused():
+    S = bq.make_scoring(SIG, choice_bias=torch.zeros(15, device=DEV))
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    R = bq.alloc_routing(2, 16, 2)
+    with pytest.raises(bq.MoeError):
+        bq.moe_route_scored(_layer(), S, None, 2, bq.MOE_LOGITS_GIVEN, R, ws)
+    for fn in (bq.moe_forward_decode_scored, bq.moe_forward_prefill_scored):
+        with pytest.raises(bq.MoeError):
+            fn(_layer(), S, None, 2, bq.MOE_LOGITS_GIVEN, R, ws, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(1, 96), (8, 96), (8, 1024), (77, 96), (900, 96), (40, 1024)])
+def test_captured_into_a_graph_and_on_another_stream(T, E):
+    k = 4
     layer = bq.make_layer(128, 128, E, k, 0, (2, 2, 2), None, 0)
     S = bq.make_scoring(SIG, n_groups=8, topk_groups=3, group_top=2)
     lg = torch.zeros((T, E), device=DEV)
