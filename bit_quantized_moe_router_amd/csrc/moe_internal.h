@@ -111,8 +111,8 @@ struct ScoreOut {
   int32_t *tiles, *ctrl;
   int32_t tm;  // rows per tile
 };
-constexpr int kScoredFewTokens = 32;  // tokens and rows that one block routes
-constexpr int kScoredFewRows = 1024;
+constexpr int kScoredFewTokens = 24;  // most tokens that one block routes
+constexpr int kScoredFewRows = kScoredFewTokens * MOE_MAX_TOPK;
 size_t scored_ws_bytes(const moe_layer* L, int T);  // scratch of launch_route_scored
 int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_routing* R,
                         uint8_t* scratch, const ScoreOut& out, void* stream);

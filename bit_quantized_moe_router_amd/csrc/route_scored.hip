@@ -524,12 +524,19 @@ __device__ __forceinline__ void write_other_slots(const ScoreOut& O, int T, int 
 }
 
 // ------------------------------------------------------------ few tokens
-// One block does everything for at most 1024 rows: the waves take the tokens
-// in turn, then (beyond 64 rows, or where the tile list is wanted; decode has
-// neither) the rows sit 64 to a wave, each wave ranks its rows among
-// themselves by ballots over the expert id's bits, and thread e sums the
-// waves' counts of expert e and scans them over the experts.  cnt is
-// [chunks][E] in LDS.
+// One block does everything: the waves take the tokens in turn, then (beyond
+// 64 rows, or where the tile list is wanted; decode has neither) the rows sit
+// 64 to a wave, each wave ranks its rows among themselves by ballots over the
+// expert id's bits, and thread e sums the waves' counts of expert e and scans
+// them over the experts.  cnt is [chunks][E] in LDS.
+//
+// Two launches against this one, back to back in a graph, top-8 of 32 / 128 /
+// 256 experts: 24 tokens 11.7 / 12.4 / 13.6 us against 9.1 / 10.0 / 11.9, 32
+// tokens 11.9 / 12.6 / 13.6 against 11.7 / 12.9 / 15.1; hence the limit of 24.
+// Beyond 256 experts a lane holds 8 or 16 values and 16 waves have too few
+// registers for them (1024 experts: 11.2 us for one token, 19.3 for eight, 39
+// for 32, against 9.8, 12.9 and 16.9 with 8 waves), so the block has 8 waves
+// and keeps to 64 rows.
 template <int PER, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float* __restrict__ logits,
                                                         int T, ScoreOut O) {
@@ -551,7 +558,7 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
     }
   }
   __syncthreads();
-  if (rows <= 64 && !O.tiles) {
+  if (PER > 4 || (rows <= 64 && !O.tiles)) {
     // at most 64 rows, one per lane of wave 0: each row's place from ballots
     // over the bits of the expert ids; thread e counts the rows of expert e and
     // of those before it
@@ -604,7 +611,7 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
   for (int i = tid; i < chunks * E; i += THREADS) cnt[i] = 0;
   __syncthreads();
   // row r = tid (+ THREADS): its rank among the rows of the same expert in its chunk
-  constexpr int RP = kScoredFewRows / THREADS;
+  constexpr int RP = THREADS == 256 ? 1 : (kScoredFewRows + THREADS - 1) / THREADS;
   int rk[RP];
 #pragma unroll
   for (int q = 0; q < RP; ++q) {
@@ -834,8 +841,8 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
   O.perm_tok = R->perm_tok;
   O.inv_row = R->inv_row;
   const int rows = T * k;
-  if (T <= kScoredFewTokens && rows <= kScoredFewRows) {
-    const int threads = E <= 256 && T <= 4 && rows <= 256 ? 256 : 1024;
+  if (E <= 256 ? T <= kScoredFewTokens : T <= 8 && rows <= 64 && !O.tiles) {
+    const int threads = E > 256 ? 512 : T <= 4 ? 256 : 1024;
     const size_t cnt = (size_t)((rows + 63) / 64) * E * 4;
     const size_t stg = (size_t)(threads / 64) * S.stage * 8;
     const size_t lds = cnt > stg ? cnt : stg;
@@ -855,16 +862,17 @@ int launch_route_scored(const moe_layer* L, const moe_scoring* C, int T, moe_rou
         BQ_FEW(2, 256);
       else
         BQ_FEW(4, 256);
+    } else if (threads == 512) {
+      if (E <= 512)
+        BQ_FEW(8, 512);
+      else
+        BQ_FEW(16, 512);
     } else if (E <= 64)
       BQ_FEW(1, 1024);
     else if (E <= 128)
       BQ_FEW(2, 1024);
-    else if (E <= 256)
-      BQ_FEW(4, 1024);
-    else if (E <= 512)
-      BQ_FEW(8, 1024);
     else
-      BQ_FEW(16, 1024);
+      BQ_FEW(4, 1024);
 #undef BQ_FEW
     return (int)hipGetLastError();
   }

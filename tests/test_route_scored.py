@@ -171,6 +171,8 @@ SHAPES = [  # T, E, k, groups, topk_groups, group_top
     (4, 64, 6, 64, 40, 1), (7, 40, 5, 8, 2, 2), (32, 256, 32, 4, 1, 2), (33, 256, 8, 8, 4, 2),
     (3, 160, 6, 8, 3, 1), (31, 1000, 12, 5, 2, 2), (32, 1024, 32, 16, 3, 2), (2, 512, 3, 32, 1, 2),
     (257, 130, 7, 13, 5, 2), (300, 64, 4, 1, 1, 1), (1237, 160, 6, 8, 3, 1), (2000, 1024, 5, 2, 1, 2),
+    (24, 256, 32, 8, 2, 2), (25, 250, 31, 5, 2, 1), (8, 1024, 8, 32, 9, 2), (8, 600, 9, 6, 2, 1),
+    (9, 513, 3, 27, 11, 2), (4, 256, 32, 8, 5, 1), (5, 200, 13, 4, 2, 2),
     (4099, 16, 2, 4, 2, 1), (4500, 256, 32, 1, 1, 1), (700, 384, 1, 3, 1, 1)]
 
 
