@@ -910,21 +910,26 @@ __global__ __launch_bounds__(256) void k_lin_join(LinArgs A, int T, int splits,
 //   some    3.8 + run * b * 0.0095 (32 rows a tile) or 0.022 (64), and the
 //           second launch (4096 x 2064, T = 77: 13.5 us; the smallest tiles of
 //           the next kernel unsplit 24.6)
-//   tiles   a step takes a latency-bound time while the CUs have a block or
-//           less and grows with the blocks beyond it (4096 x 4096: 32 x 128
-//           22 us at T = 77, 64 x 128 34.5 at 512, 64 x 256 51 at 1000,
-//           128 x 256 77 at 2048, 128 x 512 115 at 3000; each of them up to
-//           twice that one size away)
+//   tiles   3 + S steps and an epilogue.  A step takes a latency-bound time
+//           while the CUs have a block or less and grows with the blocks
+//           beyond it; of the 128-row tiles a CU takes one block at a time, so
+//           that nothing covers their epilogues.  Measured, by tile, at
+//             1000 x 4096 x 4096   42.5 us (64 x 256), 48 (64 x 128, 128 x 256), 83 (128 x 512)
+//             2048 x 4096 x 1024   34.0 (64 x 128), 37.7 (64 x 256), 49.5, 83
+//             2048 x 4096 x 4096   74.9 (128 x 256), 83 (64 x 256), 97, 98
+//             4096 x 4096 x 4096   136 (128 x 512), 148 (128 x 256), 161, 183
+//             16384 x 512 x 1024   31.1 (128 x 256), 31.9 (64 x 256), 38, 40
 // Up to 16 rows are always few (their exact weights).
 struct LinTile {
   int nrt, waves, ct;        // rows / 32, waves, columns of a wave / 32
   float floor, base, slope;  // us a step: max(floor, base + slope * b / 256)
+  float end;                 // us of epilogue for 256 blocks
 };
-constexpr LinTile kLinTiles[] = {{1, 4, 1, 0.62f, 0.30f, 0.43f},
-                                 {2, 4, 1, 0.80f, 0.33f, 0.68f},
-                                 {2, 8, 1, 0.96f, 0.40f, 1.13f},
-                                 {4, 8, 1, 1.35f, 1.00f, 1.35f},
-                                 {4, 8, 2, 2.45f, 2.30f, 1.60f}};
+constexpr LinTile kLinTiles[] = {{1, 4, 1, 0.62f, 0.27f, 0.43f, 0.9f},
+                                 {2, 4, 1, 0.77f, 0.27f, 0.62f, 1.8f},
+                                 {2, 8, 1, 1.00f, 0.05f, 1.13f, 2.6f},
+                                 {4, 8, 1, 1.32f, 0.55f, 1.55f, 5.2f},
+                                 {4, 8, 2, 2.40f, 2.00f, 1.55f, 17.0f}};
 struct LinPlan {
   int kind;  // -2 few, -1 some, else the tile's place in kLinTiles
   int rows, tiles, ncol, run, splits;  // some
@@ -963,11 +968,11 @@ static LinPlan lin_plan(int K, int N, int T) {
     const LinTile& v = kLinTiles[i];
     const long b = (long)((T + 32 * v.nrt - 1) / (32 * v.nrt)) *
                    ((N + 32 * v.ct * v.waves - 1) / (32 * v.ct * v.waves));
-    // the fullest CU sets the time; the largest tile has one block to a CU at a time
+    // the fullest CU sets the time; of the 128-row tiles it takes one block at a time
     const float f = b <= 256 ? (float)b / 256.f : (float)((b + 255) / 256);
-    float step = v.ct == 2 && f > 1.f ? (v.base + v.slope) * f : v.base + v.slope * f;
+    float step = v.nrt == 4 && f > 1.f ? (v.base + v.slope) * f : v.base + v.slope * f;
     step = step < v.floor ? v.floor : step;
-    const float c = 3.f + S * step;
+    const float c = 3.f + v.end * f + S * step;
     if (c < cost) {
       cost = c;
       best.kind = i;
