@@ -266,7 +266,7 @@ def _check(c, got):
 # The kernels: exact for few rows; chunks of K, split or not; tiles of 32, 64 and 128 rows.  The
 # shapes below reach every one of them, each with ragged rows and columns.
 ROWS = [1, 2, 4, 5, 8, 9, 16, 17, 31, 33, 64, 65, 100, 128, 129, 300]
-MANY = (3000, 4096)  # rows and columns that take the last one
+MANY = (2111, 4080)  # rows and columns that take the last one (at 256 and 384 deep)
 
 
 @pytest.mark.gpu
@@ -287,7 +287,9 @@ def test_exact_values(T, q, K, N):
                                    (23, 4096, 16), (700, 2048, 1552), (2100, 640, 4112),
                                    (8200, 256, 2064), (2945, 384, 4080), (3001, 128, 4112),
                                    (530, 512, 4112), (1030, 640, 4080), (45, 384, 4112),
-                                   (200, 4096, 1040), (220, 8192, 208)])
+                                   (200, 4096, 1040), (220, 8192, 208),
+                                   (MANY[0], 256, MANY[1]), (MANY[0], 384, MANY[1]),
+                                   (4099, 128, 1040), (1000, 256, 1040)])
 def test_exact_values_at_larger_shapes(q, T, K, N):
     c = Case(T, K, N, q, act="none", bias=True, res=True, exact=True)
     assert torch.equal(c.run(), _bf16(c.reference().astype(np.float32)))
@@ -296,7 +298,7 @@ def test_exact_values_at_larger_shapes(q, T, K, N):
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("T,K,N", [(3, 512, 160), (40, 640, 160), (90, 2048, 160), (90, 256, 4112),
-                                   (MANY[0], 128, MANY[1])])
+                                   (MANY[0], 256, MANY[1])])
 def test_epilogues(act, T, K, N):
     for q, bias, mul, res in ((1, True, False, True), (2, False, True, False),
                               (3, True, True, True)):
@@ -318,6 +320,7 @@ def test_random_values(T, K, N, q):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,K,N", [(4, 512, 96), (80, 512, 96), (20, 2048, 96), (70, 1152, 4096),
+                                   (1000, 256, 1040), (3000, 256, 1040), (4099, 128, 1040),
                                    (MANY[0], 256, MANY[1])])
 @pytest.mark.parametrize("q", [1, 2, 3])
 def test_very_small_and_very_large_scales_and_rows(T, K, N, q):
