@@ -145,6 +145,9 @@ __device__ __forceinline__ u32x4 levels_bf16(uint32_t w, uint32_t w1, const Leve
 // Operand A is x: lane l supplies row l%16, which is token
 // 16 mt + (l%16)/4 + 4 (l%4), so that accumulator register i holds tokens
 // 4i .. 4i+3 (one per lane quarter) and RI = ceil(T/4) registers do (MT = 1).
+// Bound by the latency of one pass over the packed bytes: 4.6 us for 1 x 4096 x
+// 4096 of 2 bits (5.3 MB, 1.1 TB/s; 4.0 back to back in a graph), 6.1 for
+// 8 x 4096 x 2048 of 3 bits.
 template <bool Q3, int MT, int RI, int KU>
 __global__ __launch_bounds__(512) void k_lin_few(LinArgs A, LevelK lk, int T) {
   extern __shared__ __attribute__((aligned(16))) float s_part[];  // [W][MT][16][16]
@@ -441,6 +444,14 @@ __device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][
 // scales brought to the upper end of the range by powers of two (pass 2).
 // (Giving every row its power of two beforehand took a launch of its own that
 // read and wrote all rows: 46 us of 180 at 8192 x 4096 x 2048.)
+//
+// Measured: 8192 x 4096 x 2048 131 us (1.05 PFLOP/s), 16384 x 4096 x 4096 536
+// (1.03); the matrix cores are busy in 64 and 60 % of the cycles, at the clock
+// that the power limit leaves (about 1.6 GHz).  The rest is the build of the
+// operands, 5 to 7 vector ops for each matrix-core op of 8 passes, and the
+// epilogue, which nothing covers as one block fills a CU: 17 us for 256 blocks
+// of 128 x 512.  Loading its factor's lines during the last two steps gained
+// 1.5 % at the first size and nothing at the second.
 template <int Q, int NRT, int W, int CT>
 __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, int T,
                                                         int row_tiles, int ncol) {
@@ -697,7 +708,7 @@ __global__ __launch_bounds__(64 * W, 1) void k_lin_gemm(LinArgs A, OperandK kk, 
 // once, the next chunk's while this one is multiplied), so its rows' and
 // columns' largest values are known before anything is converted: each gets
 // its power of two, and the chunk's product is brought back to scale as it is
-// added to the block's sum.
+// added to the block's sum.  77 x 4096 x 2064: 9.3 us and 2.6 for the join.
 // part: where K is split, the partial sums [split][T][N].
 constexpr int kSomeKb = 4;
 template <int Q, int NRT>

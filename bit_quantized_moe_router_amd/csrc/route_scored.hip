@@ -660,7 +660,9 @@ __global__ __launch_bounds__(THREADS) void k_scored_few(ScoreArgs S, const float
 // Block b: tokens [b * tb, (b + 1) * tb).  The waves select, then rank the
 // block's rows per expert (64-row chunks, contiguous ones to a wave, by
 // ballots), giving each row its rank among the block's rows of its expert and
-// the block's histogram.
+// the block's histogram.  Bound by the issue of the selection's instructions,
+// 690 of a wave for a token (8192 tokens of 256 experts, top-8: 16.4 us;
+// reading the logits takes 1.8).
 template <int PER, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_scored_select(ScoreArgs S,
                                                            const float* __restrict__ logits, int T,
