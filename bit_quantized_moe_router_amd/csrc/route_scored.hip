@@ -297,8 +297,19 @@ __device__ bool choose_32(const ScoreArgs& S, const float (&lg)[PER], const floa
     }
   }
   if (!cand) rank = 64;
-  // 64-bit scores that run out at 0 are ties, which logits are not
-  if (by_logit) return !__ballot(rank < k && !(l - mx > -700.f));
+  if (by_logit) {
+    // 64-bit scores that run out at 0 are ties, which logits are not
+    if (__ballot(rank < k && !(l - mx > -700.f))) return false;
+    // a logit of 2^-18 or more is 2^-42 from any other, which l - mx > -700
+    // keeps in 64 bits; smaller ones may have one score for two logits
+    if (__ballot(rank < k && fabsf(l) < 0x1p-18f)) {
+      int small = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        small += __popcll(__ballot(lane + 64 * i < E && fabsf(lg[i]) < 0x1p-18f));
+      if (small > 1) return false;
+    }
+  }
   return true;
 }
 
@@ -455,7 +466,7 @@ __device__ __forceinline__ uint64_t match_lanes(int key, int bits, uint64_t acti
 }
 
 // Exclusive scan of one value per thread over the block; `tot` holds one int
-// per wave and one more (the total, on return in every thread through `all`).
+// per wave, `all` gets the total in every thread.
 __device__ __forceinline__ int block_scan(int v, int* tot, int& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   int incl = v;

@@ -126,6 +126,11 @@ def _inputs(T, E, kind, seed):
     elif kind == "near":
         # neighbours in fp32: scores that a 32-bit evaluation cannot tell apart
         l = (1.0 + rng.integers(0, 64, (T, E)) * 2.0 ** -23).astype(np.float32)
+    elif kind == "tiny":
+        # different logits with one 64-bit score, among the largest and in the middle of a row
+        small = rng.integers(-3, 4, (T, E)).astype(np.float32) * np.float32(1e-20)
+        l = np.where(rng.random((T, E)) < 0.5, small, l)
+        l[::2] = np.minimum(l[::2], np.float32(3e-20))
     elif kind == "masked":
         l[rng.random((T, E)) < 0.6] = -np.inf
         l[0] = -np.inf
@@ -189,7 +194,7 @@ def test_routing_matches_the_plain_form(T, E, k, G, tg, gt, sigmoid, bias, renor
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("kind", ["ties", "equal", "wide", "near", "masked", "odd"])
+@pytest.mark.parametrize("kind", ["ties", "equal", "wide", "near", "tiny", "masked", "odd"])
 @pytest.mark.parametrize("T,E,k,G,tg,gt", [(6, 64, 8, 1, 1, 1), (30, 96, 8, 8, 3, 2),
                                            (130, 256, 8, 8, 4, 2), (70, 520, 9, 1, 1, 1)])
 @pytest.mark.parametrize("sigmoid", [0, 1])
