@@ -240,7 +240,7 @@ __global__ __launch_bounds__(512) void k_lin_few(LinArgs A, LevelK lk, int T) {
 // 256, bit 4 under 64, bit 6 under 16), one packed FMA gives (u - offset) * fac
 // exactly, one packed multiply by the scale (half GB%2 of sp, for both halves
 // by operand selection) rounds to fp16's 11 bits.  That rounding is exact for
-// ternary weights and at most 2^-12 of a 2- or 3-bit weight otherwise: an
+// ternary weights and at most 2^-11 of a 2- or 3-bit weight otherwise: an
 // error of about 1e-4 of the result's size, against 1.7e-3 of its rounding to
 // bf16; keeping the scales out of the operand would cost a vector FMA per
 // result and 32-group, as much time as the matrix cores'.

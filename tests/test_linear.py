@@ -219,8 +219,9 @@ def _bound(c):
       1.25 sum |x| each per group, every term rounded once in each of at most
       34 steps (2^-23, whatever the order and rounding mode), times 32 s:
       32 * 2.5 * 34 * 2^-23 A; then K/32 + 10 steps over the groups, 2^-23 S;
-    * beyond, weights rounded to 11 bits (2^-12 S; none of ternary ones) and
-      at most K steps of 2^-23 S.
+    * beyond, weights rounded to 11 bits (half a step, 2^-11 S: three times a
+      scale just above 4/3 lies just above 4 and is rounded by up to 2^-9;
+      none of ternary ones) and at most K steps of 2^-23 S.
     The activation's slope is at most 1.13 (2 |v| for relu2); its hardware
     exponential takes an argument rounded by 2^-23 |v|, so it is off by 2^-16
     relative for |v| <= 80, and by less than 2^-16 absolute beyond.  Then one
@@ -230,7 +231,7 @@ def _bound(c):
     S = x @ w.T + (0 if c.bias is None else np.abs(c.bias))
     A = x @ np.repeat(np.abs(c.scales.astype(np.float64)), 32, axis=1).T
     few = 32 * 2.5 * 34 * 2.0 ** -23 * A + (c.K / 32 + 10) * 2.0 ** -23 * S
-    e = (0 if c.q == 1 else 2.0 ** -12) * S + c.K * 2.0 ** -23 * S
+    e = (0 if c.q == 1 else 2.0 ** -11) * S + c.K * 2.0 ** -23 * S
     e = few if c.T <= 16 else np.maximum(few, e) if c.T <= 64 else e
     v = c.pre()
     a = _act64(c.act, v)
