@@ -438,8 +438,10 @@ __device__ __forceinline__ void store_tile(const LinArgs& A, f32x16 (&acc)[NRT][
 // fp16 holds a bf16 value exactly down to 2^-17 and rounds smaller ones by at
 // most 2^-24, and the operand keeps 11 bits of a weight of scale down to 2^-17.  So
 // where each row's largest value is 0 or lies in [2^-6, 2^15] and each
-// column's largest scale is 0 or in [2^-14, 2^10], plain conversion loses
-// nothing that counts.  The block learns both maxima on the way; if one is
+// column's largest scale is 0 or in [2^-14, 2^10], plain conversion changes a
+// value by at most 2^-18 of its row's largest, which does not show in a sum
+// that this largest value takes part in, rounded to bf16 (2^-8), and hardly
+// elsewhere.  The block learns both maxima on the way; if one is
 // outside, it runs the product again with each row's values and each column's
 // scales brought to the upper end of the range by powers of two (pass 2).
 // (Giving every row its power of two beforehand took a launch of its own that

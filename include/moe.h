@@ -338,8 +338,8 @@ moe_status moe_forward_prefill_scored(const moe_layer* L, const moe_scoring* S, 
  * once.  For up to 16 rows the weights enter the product exactly; beyond,
  * 2- and 3-bit weights s * (u - offset) may be rounded to fp16's 11 significant
  * bits (at most 2^-11 of a weight; ternary ones are exact), and values of x
- * below 2^-17 of their row's largest may be rounded to multiples of 2^-39 of
- * it.  An infinity or NaN in a row of x makes values of that row of out
+ * below 2^-11 of their row's largest may be rounded toward zero to multiples
+ * of 2^-18 of it.  An infinity or NaN in a row of x makes values of that row of out
  * infinite or NaN, and no others.
  * The pages name the weights' code families only; the call is this library's. */
 typedef enum {
